@@ -50,7 +50,7 @@
 extern "C" {
 #endif
 
-#define SAS_ABI_VERSION 2
+#define SAS_ABI_VERSION 3
 
 typedef enum {
   SAS_OK = 0,
@@ -116,7 +116,7 @@ size_t sas_dense_workspace_bytes(const sas_shape* shape);
 sas_status sas_workspace_init(void* workspace, size_t ws_bytes, void* stream);
 
 /* Debugging aid (synchronises `stream`): copies the device error word to *code_out (0 if no
- * device-side check failed since the last init/check; see sas_device.cuh codes 1..5), the
+ * device-side check failed since the last init/check; see sas_device.cuh codes 1..6), the
  * batch index or position it concerns to *where_out (may be NULL), clears it, and returns
  * SAS_ERR_DEVICE_CHECK if it was set, else SAS_OK. */
 sas_status sas_check_workspace(void* workspace, size_t ws_bytes, void* stream,
@@ -221,6 +221,87 @@ sas_status sas_gather_selected(const sas_shape* shape, const void* K, const void
                                const int32_t* page_table, const int32_t* seqlens,
                                const int32_t* idx, const int32_t* k, int32_t k_max, void* Kg,
                                void* Vg, int32_t* counts, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The cache around the decode step: chunks of new tokens, a decode with a window, eviction.
+ *
+ * A chunk batch holds the new tokens of every sequence one after another:
+ *   q_start [B+1] int32 (device), ascending: sequence b's T_b = q_start[b+1] - q_start[b] new
+ *     tokens are rows q_start[b] .. q_start[b+1]-1 of the batch (T_b may be 0).  seqlens already
+ *     counts them: token t of the chunk sits at position N_b - T_b + t.
+ *   n_new: rows of the batch's arrays on the host's side, q_start[B] <= n_new.  Rows outside
+ *     every sequence are neither read for a result nor written.
+ * A sequence whose q_start entries are out of order, out of [0, n_new], or that has more new
+ * tokens than N_b is skipped (its outputs stay as they were) and sets the error word.
+ * Token strides (q_stride, kv_stride) are in elements between consecutive tokens, multiples
+ * of 8, so that rows of a fused projection can be passed as they are.
+ *
+ * Window and sinks: the token at position p sees the positions j <= p with
+ *   window <= 0, or j > p - window, or j < sinks.
+ * Pages that no token of the call sees are not read; their page-table entries may be anything.
+ * Cached rows that some token of a sequence's chunk sees hold finite values; the others may
+ * hold anything, NaN and infinities among it.
+ *
+ * Each of these calls shares a workspace with the calls above under the same rule (one shape,
+ * stream-ordered, sas_workspace_init once). */
+
+/* Rows of a chunk into the caches: K, V and, unless Kproj is NULL, the projected rows.
+ *   K_new, V_new bf16 [n_new][Hkv][d], kv_stride elements apart per token (>= Hkv * d)
+ *   M      fp32 [Hkv][r][d] (NULL with Kproj NULL)
+ *   Writes rows N_b - T_b .. N_b - 1 of every (b, h); the projected rows are bit-identical to
+ *   those of sas_build_proj_cache and sas_append_proj.
+ *   workspace: device checks are reported in its error word; NULL: they are not reported. */
+sas_status sas_append_chunk(const sas_shape* shape, const void* K_new, const void* V_new, int64_t kv_stride,
+                            const int32_t* q_start, int32_t n_new, const float* M, void* K, void* V, void* Kproj,
+                            const int32_t* page_table, const int32_t* seqlens, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/* Causal attention of a chunk of new tokens over the cache (which holds the chunk's own rows
+ * already, see sas_append_chunk), with a window and sinks as above.
+ *   q      bf16 [n_new][Hq][d], q_stride elements apart per token (>= Hq * d)
+ *   out    bf16 [n_new][Hq][d], written; the softmax weights enter the second product rounded
+ *          to bf16, sums and statistics are fp32
+ *   lse    fp32 [n_new][Hq] or NULL, written: log sum_j exp(sigma q . K_j) over the visible j
+ *   Hq / Hkv <= 128.
+ *   workspace: sas_chunk_workspace_bytes(shape, n_new) bytes. */
+size_t sas_chunk_workspace_bytes(const sas_shape* shape, int32_t n_new);
+sas_status sas_chunk_attention(const sas_shape* shape, const void* q, int64_t q_stride, const int32_t* q_start,
+                               int32_t n_new, const void* K, const void* V, const int32_t* page_table,
+                               const int32_t* seqlens, int32_t window, int32_t sinks, void* out, float* lse,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* Decode of the newest token of every sequence (position N_b - 1) with a window and sinks, in
+ * fp32 like sas_dense_decode, which it equals without a window.
+ *   q       bf16 [B][Hq][d];  out fp32 [B][Hq][d], written (zeros where N_b == 0)
+ *   lse     fp32 [B][Hq] or NULL, written (-infinity where N_b == 0)
+ *   weights fp32 [B][Hkv][cap] or NULL: the softmax weights of the group's heads are added,
+ *           weights[b,h,j] += sum_g softmax_g(j) for the visible j; the others keep their value.
+ *   workspace: sas_window_workspace_bytes(shape, weights != NULL) bytes. */
+size_t sas_window_workspace_bytes(const sas_shape* shape, int32_t with_weights);
+sas_status sas_window_decode(const sas_shape* shape, const void* q, const void* K, const void* V,
+                             const int32_t* page_table, const int32_t* seqlens, int32_t window, int32_t sinks,
+                             float* out, float* lse, float* weights, void* workspace, size_t ws_bytes, void* stream);
+
+/* Eviction by accumulated weight: every (b, h) keeps min(N_b, keep_b) of its rows and moves
+ * them, in order, to positions 0 .. of its cache.  Kept are, in this order until keep_b are
+ * found: positions < sinks (lowest first), the newest `recent` positions (newest first), then
+ * the largest weights (ties to the lower position; a NaN weight counts as the least).
+ *   weights     fp32 [B][Hkv][cap], read
+ *   keep        int32 [B] (device), keep_max its bound on the host (>= 1); a value over it is
+ *               clamped and sets the error word, one below 0 counts as 0
+ *   K, V        caches, moved in place; Kproj, log_g: moved too unless NULL
+ *   idx_out     int32 [B][Hkv][keep_max], written: the kept positions, ascending, then -1
+ *   weights_out fp32 [B][Hkv][cap], written: the kept weights, then zeros up to N_b
+ *   seqlens_out int32 [B], written: min(N_b, keep_b)
+ *   weights_out may be weights and seqlens_out may be seqlens (in place); other overlaps of
+ *   arguments are not allowed.  No page may belong to two entries of the page table.
+ *   Rows at and behind the new length stay as they were.
+ *   workspace: sas_evict_workspace_bytes(shape, keep_max) bytes. */
+size_t sas_evict_workspace_bytes(const sas_shape* shape, int32_t keep_max);
+sas_status sas_evict(const sas_shape* shape, const float* weights, const int32_t* keep, int32_t keep_max,
+                     int32_t sinks, int32_t recent, void* K, void* V, void* Kproj, float* log_g,
+                     const int32_t* page_table, const int32_t* seqlens, int32_t* idx_out, float* weights_out,
+                     int32_t* seqlens_out, void* workspace, size_t ws_bytes, void* stream);
 
 /* Bytes of the library's fixed scratch array (16 MiB), used by sas_decode_step_static_scratch. */
 #define SAS_STATIC_SCRATCH_BYTES (16u << 20)

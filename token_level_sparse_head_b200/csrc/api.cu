@@ -96,6 +96,48 @@ cudaError_t prepare_kernel(const void* kern, int smem_bytes, bool nonportable_cl
   return e;
 }
 
+namespace {
+using PfnEncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+PfnEncodeTiled encode_tiled() {
+  static const PfnEncodeTiled fn = [] {
+    PfnEncodeTiled f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", reinterpret_cast<void**>(&f), cudaEnableDefault, &q) !=
+            cudaSuccess || q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return f;
+  }();
+  return fn;
+}
+
+cudaError_t encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box) {
+  const PfnEncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides,
+                        box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+}  // namespace
+
+cudaError_t rows_map(CUtensorMap* map, const void* base, unsigned long long rows, int d, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)d, rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  return encode(map, base, 2, dims, strides, box);
+}
+
+cudaError_t q_map(CUtensorMap* map, const void* q, long long stride, int n_new, int Hq, int G, int d, int tok) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)Hq, (cuuint64_t)n_new};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tok};
+  return encode(map, q, 3, dims, strides, box);
+}
+
 int ctas_per_sm(const void* kern, int threads, int smem_bytes) {
   struct Key {
     const void* k;
@@ -569,6 +611,261 @@ sas_status sas_gather_selected(const sas_shape* shape, const void* K, const void
   p.k_max = k_max;
   const cudaError_t e = sas::launch_gather(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SAS_OK : cuda_fail(e, "gather kernel launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// The cache around the decode step: chunk append, chunk attention, window decode, eviction.  Their
+// scratch lies behind the error word and the histograms, which every call on a workspace shares
+// and the selection leaves zero.
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+size_t scratch_offset(const sas_shape* s) { return kErrBytes + (size_t)s->B * s->Hkv * sas::kHistBins * 4; }
+
+// Rows of the K and V caches (the first row past them reads as zeros through a tensor map).
+long long cache_rows(const sas_shape* s) {
+  return s->page_size ? (long long)s->num_pages * s->Hkv * 64 : (long long)s->B * s->Hkv * s->n_cap;
+}
+
+sas_status check_map_rows(const sas_shape* s) {
+  if (cache_rows(s) >= (1LL << 31) - 64) return fail(SAS_ERR_UNSUPPORTED, "cache rows exceed 2^31 - 64");
+  return SAS_OK;
+}
+
+sas_status check_stride(long long stride, long long least, const char* name) {
+  if (stride < least || (stride % 8) || stride >= (1LL << 38))
+    return fail(SAS_ERR_INVALID_ARG, "%s (%lld) must be a multiple of 8, at least %lld and below 2^38", name, stride, least);
+  return SAS_OK;
+}
+
+sas_status check_ws(const void* ws, size_t have, size_t need) {
+  SAS_TRY(check_ptr(ws, "workspace"));
+  if (have < need) return fail(SAS_ERR_INVALID_ARG, "workspace too small: %zu bytes, %zu needed", have, need);
+  return SAS_OK;
+}
+
+sas_status check_chunk_args(const sas_shape* s, int32_t n_new) {
+  SAS_TRY(check_shape(s));
+  if (n_new < 1) return fail(SAS_ERR_INVALID_ARG, "n_new must be >= 1");
+  if (n_new > (1 << 22)) return fail(SAS_ERR_UNSUPPORTED, "n_new=%d exceeds 2^22", n_new);
+  return SAS_OK;
+}
+
+int shared_ctas() {
+  const int n = num_sms();
+  return n < sas::kChunkMaxCtas ? n : sas::kChunkMaxCtas;
+}
+
+sas::ChunkParams chunk_plan(const sas_shape* s, int32_t n_new) {
+  sas::ChunkParams p = {};
+  p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.G = s->Hq / s->Hkv; p.d = s->d; p.cap = cap_of(s);
+  p.max_pages = s->max_pages; p.num_pages = s->num_pages; p.paged = s->page_size ? 1 : 0;
+  p.n_new = n_new;
+  sas::plan_chunk(p);
+  return p;
+}
+
+sas::WindowParams window_plan(const sas_shape* s, int32_t window, int32_t sinks) {
+  sas::WindowParams p = {};
+  p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.G = s->Hq / s->Hkv; p.d = s->d; p.cap = cap_of(s);
+  p.max_pages = s->max_pages; p.num_pages = s->num_pages; p.paged = s->page_size ? 1 : 0;
+  p.window = window > 0 ? window : 0;
+  p.sinks = sinks;
+  sas::plan_window(p);
+  return p;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+}  // namespace
+
+extern "C" {
+
+sas_status sas_append_chunk(const sas_shape* shape, const void* K_new, const void* V_new, int64_t kv_stride,
+                            const int32_t* q_start, int32_t n_new, const float* M, void* K, void* V, void* Kproj,
+                            const int32_t* page_table, const int32_t* seqlens, void* workspace, size_t ws_bytes,
+                            void* stream) {
+  SAS_TRY(check_chunk_args(shape, n_new));
+  SAS_TRY(check_ptr(K_new, "K_new"));
+  SAS_TRY(check_ptr(V_new, "V_new"));
+  SAS_TRY(check_stride(kv_stride, (long long)shape->Hkv * shape->d, "kv_stride"));
+  SAS_TRY(check_ptr(q_start, "q_start"));
+  SAS_TRY(check_ptr(K, "K"));
+  SAS_TRY(check_ptr(V, "V"));
+  SAS_TRY(check_ptr(Kproj, "Kproj", false));
+  if (Kproj != nullptr) SAS_TRY(check_ptr(M, "M"));
+  SAS_TRY(check_cache_ptrs(shape, page_table, seqlens));
+  if (workspace != nullptr) SAS_TRY(check_ws(workspace, ws_bytes, kErrBytes));
+  sas::AppendParams p = {};
+  p.K_new = static_cast<const __nv_bfloat16*>(K_new);
+  p.V_new = static_cast<const __nv_bfloat16*>(V_new);
+  p.kv_stride = kv_stride;
+  p.q_start = q_start;
+  p.M = M;
+  p.K = static_cast<__nv_bfloat16*>(K);
+  p.V = static_cast<__nv_bfloat16*>(V);
+  p.Kproj = Kproj;
+  p.kproj_scale = shape->kproj_scale;
+  p.page_table = shape->page_size ? page_table : nullptr;
+  p.seqlens = seqlens;
+  p.err = static_cast<uint32_t*>(workspace);
+  p.B = shape->B; p.Hkv = shape->Hkv; p.d = shape->d; p.r = shape->r; p.cap = cap_of(shape);
+  p.max_pages = shape->max_pages; p.num_pages = shape->num_pages; p.paged = shape->page_size ? 1 : 0;
+  p.fp8 = shape->kproj_dtype == SAS_KPROJ_FP8_E4M3 ? 1 : 0;
+  p.n_new = n_new;
+  const cudaError_t e = sas::launch_append_chunk(p, num_sms(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAS_OK : cuda_fail(e, "chunk append launch");
+}
+
+size_t sas_chunk_workspace_bytes(const sas_shape* shape, int32_t n_new) {
+  if (check_chunk_args(shape, n_new) != SAS_OK || shape->Hq / shape->Hkv > 128) return 0;
+  return scratch_offset(shape) + sas::chunk_workspace_bytes(chunk_plan(shape, n_new));
+}
+
+sas_status sas_chunk_attention(const sas_shape* shape, const void* q, int64_t q_stride, const int32_t* q_start,
+                               int32_t n_new, const void* K, const void* V, const int32_t* page_table,
+                               const int32_t* seqlens, int32_t window, int32_t sinks, void* out, float* lse,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  SAS_TRY(check_chunk_args(shape, n_new));
+  if (shape->Hq / shape->Hkv > 128) return fail(SAS_ERR_UNSUPPORTED, "Hq / Hkv = %d exceeds 128", shape->Hq / shape->Hkv);
+  if (sinks < 0) return fail(SAS_ERR_INVALID_ARG, "sinks must be >= 0");
+  SAS_TRY(check_map_rows(shape));
+  SAS_TRY(check_ptr(q, "q"));
+  SAS_TRY(check_stride(q_stride, (long long)shape->Hq * shape->d, "q_stride"));
+  SAS_TRY(check_ptr(q_start, "q_start"));
+  SAS_TRY(check_ptr(K, "K"));
+  SAS_TRY(check_ptr(V, "V"));
+  SAS_TRY(check_ptr(out, "out"));
+  SAS_TRY(check_ptr(lse, "lse", false));
+  SAS_TRY(check_cache_ptrs(shape, page_table, seqlens));
+  SAS_TRY(check_ws(workspace, ws_bytes, sas_chunk_workspace_bytes(shape, n_new)));
+  sas::ChunkParams p = chunk_plan(shape, n_new);
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  sas::bind_chunk(p, w + scratch_offset(shape));
+  p.q_start = q_start;
+  p.page_table = shape->page_size ? page_table : nullptr;
+  p.seqlens = seqlens;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.err = reinterpret_cast<uint32_t*>(w);
+  p.window = window > 0 ? window : 0;
+  p.sinks = sinks;
+  p.ctas = shared_ctas();
+  p.row_end = (int)cache_rows(shape);
+  p.scale_log2 = kLog2e / sqrtf((float)shape->d);
+  cudaError_t e = sas::q_map(&p.qmap, q, q_stride, n_new, p.Hq, p.G, p.d, p.tok_tile);
+  if (e == cudaSuccess) e = sas::rows_map(&p.kmap, K, (unsigned long long)p.row_end, p.d, 64);
+  if (e == cudaSuccess) e = sas::rows_map(&p.vmap, V, (unsigned long long)p.row_end, p.d, 64);
+  if (e != cudaSuccess) return cuda_fail(e, "tensor maps of the chunk attention");
+  e = sas::launch_chunk(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAS_OK : cuda_fail(e, "chunk attention launch");
+}
+
+size_t sas_window_workspace_bytes(const sas_shape* shape, int32_t with_weights) {
+  if (check_shape(shape) != SAS_OK) return 0;
+  return scratch_offset(shape) + sas::window_workspace_bytes(window_plan(shape, 0, 0), with_weights != 0);
+}
+
+sas_status sas_window_decode(const sas_shape* shape, const void* q, const void* K, const void* V,
+                             const int32_t* page_table, const int32_t* seqlens, int32_t window, int32_t sinks,
+                             float* out, float* lse, float* weights, void* workspace, size_t ws_bytes, void* stream) {
+  SAS_TRY(check_shape(shape));
+  if (sinks < 0) return fail(SAS_ERR_INVALID_ARG, "sinks must be >= 0");
+  SAS_TRY(check_map_rows(shape));
+  SAS_TRY(check_ptr(q, "q"));
+  SAS_TRY(check_ptr(K, "K"));
+  SAS_TRY(check_ptr(V, "V"));
+  SAS_TRY(check_ptr(out, "out"));
+  SAS_TRY(check_ptr(lse, "lse", false));
+  SAS_TRY(check_ptr(weights, "weights", false));
+  SAS_TRY(check_cache_ptrs(shape, page_table, seqlens));
+  SAS_TRY(check_ws(workspace, ws_bytes, sas_window_workspace_bytes(shape, weights != nullptr)));
+  sas::WindowParams p = window_plan(shape, window, sinks);
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  sas::bind_window(p, w + scratch_offset(shape), weights != nullptr);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.page_table = shape->page_size ? page_table : nullptr;
+  p.seqlens = seqlens;
+  p.out = out;
+  p.lse = lse;
+  p.weights = weights;
+  p.err = reinterpret_cast<uint32_t*>(w);
+  p.ctas = shared_ctas();
+  p.row_end = (int)cache_rows(shape);
+  p.scale_log2 = kLog2e / sqrtf((float)shape->d);
+  cudaError_t e = sas::rows_map(&p.kmap, K, (unsigned long long)p.row_end, p.d, 64);
+  if (e == cudaSuccess) e = sas::rows_map(&p.vmap, V, (unsigned long long)p.row_end, p.d, 64);
+  if (e != cudaSuccess) return cuda_fail(e, "tensor maps of the window decode");
+  e = sas::launch_window(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAS_OK : cuda_fail(e, "window decode launch");
+}
+
+size_t sas_evict_workspace_bytes(const sas_shape* shape, int32_t keep_max) {
+  if (check_shape(shape) != SAS_OK || keep_max < 1) return 0;
+  return scratch_offset(shape) + (((size_t)shape->B * sizeof(int2) + 255) & ~(size_t)255) +
+         (size_t)shape->B * shape->Hkv * cap_of(shape) * 4;
+}
+
+sas_status sas_evict(const sas_shape* shape, const float* weights, const int32_t* keep, int32_t keep_max,
+                     int32_t sinks, int32_t recent, void* K, void* V, void* Kproj, float* log_g,
+                     const int32_t* page_table, const int32_t* seqlens, int32_t* idx_out, float* weights_out,
+                     int32_t* seqlens_out, void* workspace, size_t ws_bytes, void* stream) {
+  SAS_TRY(check_shape(shape));
+  if (keep_max < 1) return fail(SAS_ERR_INVALID_ARG, "keep_max must be >= 1");
+  if (sinks < 0 || recent < 0) return fail(SAS_ERR_INVALID_ARG, "sinks and recent must be >= 0");
+  SAS_TRY(check_ptr(weights, "weights"));
+  SAS_TRY(check_ptr(keep, "keep"));
+  SAS_TRY(check_ptr(K, "K"));
+  SAS_TRY(check_ptr(V, "V"));
+  SAS_TRY(check_ptr(Kproj, "Kproj", false));
+  SAS_TRY(check_ptr(log_g, "log_g", false));
+  SAS_TRY(check_cache_ptrs(shape, page_table, seqlens));
+  SAS_TRY(check_ptr(idx_out, "idx_out"));
+  SAS_TRY(check_ptr(weights_out, "weights_out"));
+  SAS_TRY(check_ptr(seqlens_out, "seqlens_out"));
+  SAS_TRY(check_ws(workspace, ws_bytes, sas_evict_workspace_bytes(shape, keep_max)));
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  unsigned char* scratch = w + scratch_offset(shape);
+  sas::EvictParams p = {};
+  p.weights = weights;
+  p.keep = keep;
+  p.seqlens = seqlens;
+  p.page_table = shape->page_size ? page_table : nullptr;
+  p.K = static_cast<unsigned char*>(K);
+  p.V = static_cast<unsigned char*>(V);
+  p.Kproj = static_cast<unsigned char*>(Kproj);
+  p.log_g = log_g;
+  p.idx = idx_out;
+  p.weights_out = weights_out;
+  p.seqlens_out = seqlens_out;
+  p.err = reinterpret_cast<uint32_t*>(w);
+  p.hist = reinterpret_cast<uint32_t*>(w + kErrBytes);
+  p.plan = reinterpret_cast<int2*>(scratch);
+  p.keys = reinterpret_cast<uint32_t*>(scratch + (((size_t)shape->B * sizeof(int2) + 255) & ~(size_t)255));
+  p.B = shape->B; p.Hkv = shape->Hkv; p.cap = cap_of(shape);
+  p.max_pages = shape->max_pages; p.num_pages = shape->num_pages; p.paged = shape->page_size ? 1 : 0;
+  p.keep_max = keep_max; p.sinks = sinks; p.recent = recent;
+  p.row_bytes = shape->d * 2;
+  p.proj_bytes = shape->r * (shape->kproj_dtype == SAS_KPROJ_FP8_E4M3 ? 1 : 2);
+
+  sas::SelectParams sl = {};
+  sl.keys = p.keys;
+  sl.hist = p.hist;
+  sl.seqlens = seqlens;
+  sl.kvec = keep;
+  sl.idx_out = idx_out;
+  sl.err = p.err;
+  sl.B = shape->B; sl.Hkv = shape->Hkv; sl.cap = p.cap; sl.k_max = keep_max;
+  if (!sas::plan_select(sl, num_sms())) return fail(SAS_ERR_UNSUPPORTED, "no selection plan for this shape");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = sas::launch_evict_keys(p, st);
+  if (e != cudaSuccess) return cuda_fail(e, "eviction keys launch");
+  e = sas::launch_select(sl, st);
+  if (e != cudaSuccess) return cuda_fail(e, "select kernel launch");
+  e = sas::launch_evict_move(p, st);
+  return e == cudaSuccess ? SAS_OK : cuda_fail(e, "eviction move launch");
 }
 
 }  // extern "C"

@@ -20,6 +20,7 @@ enum DeviceError : uint32_t {
   kDevBadIndex = 3,      // an index list entry outside [0, N_b)
   kDevKOverMax = 4,      // k[b] > k_max (clamped to k_max)
   kDevWaitTimeout = 5,   // a bounded mbarrier wait ran out
+  kDevBadChunk = 6,      // q_start out of order or range, or more new tokens than N_b
 };
 
 __device__ __forceinline__ void record_error(uint32_t* err, uint32_t code, uint32_t where) {
@@ -58,6 +59,23 @@ __device__ __forceinline__ SeqSelection seq_selection(int kb, int n) {
   s.k_eff = max(0, min(kb, n));
   s.ranked = (kb > 0) && (n > 0) && (kb < n);
   return s;
+}
+
+// ----------------------------------------------------------------------------- visible pages
+// The 64-row pages that the positions p_lo .. p_hi of one sequence see: the sinks' pages that lie
+// before the window, then the window's.  Virtual page v of nv is page(v) of the sequence.
+struct VisiblePages {
+  int ns, w0, nv;  // sink pages, first window page, all pages
+  int first;       // lowest position of the window of p_lo
+  __device__ __forceinline__ int page(int v) const { return v < ns ? v : v - ns + w0; }
+};
+__device__ __forceinline__ VisiblePages visible_pages(int p_lo, int p_hi, int window, int sinks) {
+  VisiblePages x;
+  x.first = window > 0 ? max(0, p_lo - window + 1) : 0;
+  x.w0 = x.first >> 6;
+  x.ns = min((min(max(sinks, 0), x.first) + 63) >> 6, x.w0);
+  x.nv = x.ns + (p_hi >> 6) + 1 - x.w0;
+  return x;
 }
 
 // ----------------------------------------------------------------------------- PTX
@@ -108,6 +126,29 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   for (uint32_t i = 0; i < kWaitLimit; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
+}
+
+// Tiled bulk copy of a 2D / 3D tensor-map box; x is a multiple of 8 bf16 elements.  A box that
+// starts past the last row reads zeros.
+__device__ __forceinline__ void tma_2d(void* dst, const void* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Global -> this CTA's shared memory bulk copy on the TMA engine; completion is signalled

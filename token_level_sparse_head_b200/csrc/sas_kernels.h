@@ -4,6 +4,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda_bf16.h>
+#include <cuda.h>  // CUtensorMap
 #include <cuda_runtime.h>
 
 namespace sas {
@@ -117,6 +118,113 @@ struct AttendParams {
 void plan_attend(AttendParams& p, int count_max, bool dense);
 size_t attend_workspace_floats(const AttendParams& p);
 cudaError_t launch_attend(const AttendParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------- chunk append
+struct AppendParams {
+  const __nv_bfloat16* K_new;  // [n_new][Hkv][d], kv_stride elements per token
+  const __nv_bfloat16* V_new;
+  long long kv_stride;
+  const int32_t* q_start;      // [B+1]
+  const float* M;              // [Hkv][r][d] or null
+  __nv_bfloat16* K;            // cache layout
+  __nv_bfloat16* V;
+  void* Kproj;                 // cache layout, width r, or null
+  const float* kproj_scale;
+  const int32_t* page_table;
+  const int32_t* seqlens;
+  uint32_t* err;
+  int B, Hkv, d, r, cap, max_pages, num_pages, paged, fp8, n_new;
+};
+cudaError_t launch_append_chunk(const AppendParams& p, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------- chunk attention
+// One task: up to two tiles of tokens of one sequence, and the units (blocks of 128 keys) before it.
+struct ChunkTask {
+  int32_t b, tok0, ntok, pos0;  // sequence, first row of q, tokens, position of the first
+  long long unit0;              // units of the tasks before this one (one KV head)
+  int32_t blocks, pad;
+};
+struct ChunkParams {
+  CUtensorMap qmap, kmap, vmap;
+  const int32_t* q_start;
+  const int32_t* page_table;
+  const int32_t* seqlens;
+  __nv_bfloat16* out;          // [n_new][Hq][d]
+  float* lse;                  // [n_new][Hq] or null
+  uint32_t* err;
+  ChunkTask* tasks;            // workspace: [slots] then the total of the units in tasks[slots].unit0
+  float* part;                 // workspace: [2 * ctas][d / 4][rows_cap] float4
+  float2* ml;                  // workspace: [2 * ctas][rows_cap] (running maximum, sum)
+  int B, Hq, Hkv, G, d, cap, max_pages, num_pages, paged, n_new;
+  int window, sinks;
+  int slots, tok_tile;         // task slots; tokens per 128-row tile
+  int rows_cap;                // rows of a partial
+  int ctas;                    // CTAs that share the units
+  int row_end;                 // rows of the K / V tensor maps (a box there reads zeros)
+  float scale_log2;            // sigma * log2(e)
+};
+constexpr int kChunkMaxCtas = 160;   // CTAs the chunk and window workspaces hold partials for
+void plan_chunk(ChunkParams& p);
+size_t chunk_workspace_bytes(const ChunkParams& p);
+void bind_chunk(ChunkParams& p, void* scratch);
+cudaError_t launch_chunk(const ChunkParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------- window decode
+struct WindowDesc {            // where a CTA's share of the pages begins
+  int32_t b, h, hg, page, nv, pad[3];
+};
+struct WindowParams {
+  CUtensorMap kmap, vmap;
+  const __nv_bfloat16* q;      // [B][Hq][d]
+  const int32_t* page_table;
+  const int32_t* seqlens;
+  float* out;                  // [B][Hq][d]
+  float* lse;                  // [B][Hq] or null
+  float* weights;              // [B][Hkv][cap] or null
+  uint32_t* err;
+  WindowDesc* desc;            // workspace: [ctas + 1] (the last: total pages in page, share in nv)
+  float* part;                 // workspace: [2 * ctas][16][d]
+  float2* ml;                  // workspace: [2 * ctas][16]
+  float* lse2;                 // workspace: [B][Hq] base-2 log of the sums (with weights)
+  float* z;                    // workspace: [B][Hkv][zcap][gpad] base-2 logits by virtual position (with weights)
+  int B, Hq, Hkv, G, d, cap, max_pages, num_pages, paged;
+  int window, sinks;
+  int hgs, gpad, zcap;         // head groups of up to 16; heads per row of z; rows of z
+  int ctas, row_end;
+  float scale_log2;
+};
+void plan_window(WindowParams& p);
+size_t window_workspace_bytes(const WindowParams& p, bool weights);
+void bind_window(WindowParams& p, void* scratch, bool weights);
+cudaError_t launch_window(const WindowParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------- eviction
+struct EvictParams {
+  const float* weights;        // [B][Hkv][cap]
+  const int32_t* keep;         // [B]
+  const int32_t* seqlens;
+  const int32_t* page_table;
+  unsigned char* K;
+  unsigned char* V;
+  unsigned char* Kproj;        // or null
+  float* log_g;                // or null
+  const int32_t* idx;          // [B][Hkv][keep_max]
+  float* weights_out;
+  int32_t* seqlens_out;
+  uint32_t* keys;              // workspace: [B][Hkv][cap]
+  uint32_t* hist;              // workspace: [B][Hkv][kHistBins]
+  int2* plan;                  // workspace: [B] (N_b, rows kept)
+  uint32_t* err;
+  int B, Hkv, cap, max_pages, num_pages, paged, keep_max, sinks, recent;
+  int row_bytes, proj_bytes;   // bytes of a K row and of a projected row
+};
+cudaError_t launch_evict_keys(const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t stream);
+
+// 2D map of bf16 rows [rows][d] read in boxes of 64 columns (128 swizzled bytes) by box_rows rows.
+cudaError_t rows_map(CUtensorMap* map, const void* base, unsigned long long rows, int d, int box_rows);
+// 3D map of q [tokens][Hq][d] read in boxes of 64 columns by G heads by tok tokens.
+cudaError_t q_map(CUtensorMap* map, const void* q, long long stride, int n_new, int Hq, int G, int d, int tok);
 
 // Raises a kernel's dynamic shared-memory limit (and allows non-portable cluster sizes) on the
 // current device once, not on every launch; thread-safe.

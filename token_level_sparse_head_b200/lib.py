@@ -19,7 +19,7 @@ SAS_OK, SAS_ERR_INVALID_ARG, SAS_ERR_UNSUPPORTED, SAS_ERR_CUDA, SAS_ERR_DEVICE_C
 PAGE_SIZE = 64
 
 # Exported symbols and their C signatures (kept in step with include/sas.h).
-_vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 
 
 class sas_shape(ctypes.Structure):
@@ -57,6 +57,17 @@ _SIGS = {
                                                       _vp, _vp, _i32, _f32, _vp, _vp, _vp, _vp]),
     "sas_gather_selected": (ctypes.c_int, [ctypes.POINTER(sas_shape), _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
                                            _vp, _vp]),
+    "sas_append_chunk": (ctypes.c_int, [ctypes.POINTER(sas_shape), _vp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp,
+                                        _vp, _vp, _vp, _sz, _vp]),
+    "sas_chunk_workspace_bytes": (_sz, [ctypes.POINTER(sas_shape), _i32]),
+    "sas_chunk_attention": (ctypes.c_int, [ctypes.POINTER(sas_shape), _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _i32,
+                                           _i32, _vp, _vp, _vp, _sz, _vp]),
+    "sas_window_workspace_bytes": (_sz, [ctypes.POINTER(sas_shape), _i32]),
+    "sas_window_decode": (ctypes.c_int, [ctypes.POINTER(sas_shape), _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp,
+                                         _vp, _vp, _sz, _vp]),
+    "sas_evict_workspace_bytes": (_sz, [ctypes.POINTER(sas_shape), _i32]),
+    "sas_evict": (ctypes.c_int, [ctypes.POINTER(sas_shape), _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 STATIC_SCRATCH_BYTES = 16 << 20  # SAS_STATIC_SCRATCH_BYTES
 EXPORTED = tuple(_SIGS)
@@ -242,3 +253,49 @@ def sas_gather_selected(shape: Shape, K, V, page_table, seqlens, idx, k, k_max: 
     _check(load().sas_gather_selected(ctypes.byref(shape.c()), _p(K), _p(V), _p(page_table), _p(seqlens), _p(idx),
                                       _p(k), int(k_max), _p(Kg), _p(Vg), _p(counts), _stream(stream)),
            "sas_gather_selected")
+
+
+# ------------------------------------------------------------------------------ the cache around the step
+def sas_append_chunk(shape: Shape, K_new, V_new, kv_stride: int, q_start, n_new: int, M, K, V, Kproj, page_table,
+                     seqlens, workspace=None, ws_bytes: int = 0, stream=None):
+    """Rows of a chunk of new tokens into K, V and (unless Kproj is None) the projected cache."""
+    _check(load().sas_append_chunk(ctypes.byref(shape.c()), _p(K_new), _p(V_new), int(kv_stride), _p(q_start),
+                                   int(n_new), _p(M), _p(K), _p(V), _p(Kproj), _p(page_table), _p(seqlens),
+                                   _p(workspace), int(ws_bytes), _stream(stream)), "sas_append_chunk")
+
+
+def sas_chunk_workspace_bytes(shape: Shape, n_new: int) -> int:
+    return int(load().sas_chunk_workspace_bytes(ctypes.byref(shape.c()), int(n_new)))
+
+
+def sas_chunk_attention(shape: Shape, q, q_stride: int, q_start, n_new: int, K, V, page_table, seqlens, window: int,
+                        sinks: int, out, lse, workspace, ws_bytes: int, stream=None):
+    """Causal attention of a chunk of new tokens over the cache, with a window and sinks."""
+    _check(load().sas_chunk_attention(ctypes.byref(shape.c()), _p(q), int(q_stride), _p(q_start), int(n_new), _p(K),
+                                      _p(V), _p(page_table), _p(seqlens), int(window), int(sinks), _p(out), _p(lse),
+                                      _p(workspace), int(ws_bytes), _stream(stream)), "sas_chunk_attention")
+
+
+def sas_window_workspace_bytes(shape: Shape, with_weights: bool) -> int:
+    return int(load().sas_window_workspace_bytes(ctypes.byref(shape.c()), int(with_weights)))
+
+
+def sas_window_decode(shape: Shape, q, K, V, page_table, seqlens, window: int, sinks: int, out, lse, weights,
+                      workspace, ws_bytes: int, stream=None):
+    """Decode of the newest token with a window and sinks; adds the softmax weights to `weights` unless None."""
+    _check(load().sas_window_decode(ctypes.byref(shape.c()), _p(q), _p(K), _p(V), _p(page_table), _p(seqlens),
+                                    int(window), int(sinks), _p(out), _p(lse), _p(weights), _p(workspace),
+                                    int(ws_bytes), _stream(stream)), "sas_window_decode")
+
+
+def sas_evict_workspace_bytes(shape: Shape, keep_max: int) -> int:
+    return int(load().sas_evict_workspace_bytes(ctypes.byref(shape.c()), int(keep_max)))
+
+
+def sas_evict(shape: Shape, weights, keep, keep_max: int, sinks: int, recent: int, K, V, Kproj, log_g, page_table,
+              seqlens, idx_out, weights_out, seqlens_out, workspace, ws_bytes: int, stream=None):
+    """Keeps the sinks, the newest rows and the largest weights of every (b, h), moved down in place."""
+    _check(load().sas_evict(ctypes.byref(shape.c()), _p(weights), _p(keep), int(keep_max), int(sinks), int(recent),
+                            _p(K), _p(V), _p(Kproj), _p(log_g), _p(page_table), _p(seqlens), _p(idx_out),
+                            _p(weights_out), _p(seqlens_out), _p(workspace), int(ws_bytes), _stream(stream)),
+           "sas_evict")

@@ -10,17 +10,41 @@ import torch
 from . import lib
 
 
-class DecodeSession:
-    """Workspace + output buffers for repeated decode steps of one shape and budget bound."""
+def _tokens(x, heads: int, d: int, name: str):
+    """Tokens and token stride of a bf16 [n][heads][d] tensor whose heads are dense."""
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d:
+        raise ValueError(f"{name} must be bf16 [tokens][{heads}][{d}], got {x.dtype} {tuple(x.shape)}")
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a token must lie one after another")
+    n = x.shape[0]
+    return n, x.stride(0) if n > 1 else max(x.stride(0), heads * d)
 
-    def __init__(self, shape: lib.Shape, k_max: int, device="cuda", dense: bool = True):
+
+class DecodeSession:
+    """Workspace + output buffers for repeated decode steps of one shape and budget bound.
+
+    chunk: the most new tokens a call of chunk() takes (0: chunk() is not used).
+    window, weights: window() is used, and whether with accumulated weights.
+    evict: evict() is used, with budgets of at most k_max rows.
+    """
+
+    def __init__(self, shape: lib.Shape, k_max: int, device="cuda", dense: bool = True, chunk: int = 0,
+                 window: bool = False, weights: bool = False, evict: bool = False):
         self.shape = shape
         self.k_max = int(k_max)
-        nbytes = lib.sas_decode_workspace_bytes(shape, self.k_max)
+        self.chunk_max = int(chunk)
+        sizes = [lib.sas_decode_workspace_bytes(shape, self.k_max)]
         if dense:
-            nbytes = max(nbytes, lib.sas_dense_workspace_bytes(shape))
-        if nbytes == 0:
+            sizes.append(lib.sas_dense_workspace_bytes(shape))
+        if chunk:
+            sizes.append(lib.sas_chunk_workspace_bytes(shape, self.chunk_max))
+        if window or weights:
+            sizes.append(lib.sas_window_workspace_bytes(shape, weights))
+        if evict:
+            sizes.append(lib.sas_evict_workspace_bytes(shape, self.k_max))
+        if min(sizes) == 0:
             raise ValueError("invalid shape for libsas")
+        nbytes = max(sizes)
         self.ws_bytes = nbytes
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         lib.sas_workspace_init(self.workspace, nbytes)
@@ -50,6 +74,40 @@ class DecodeSession:
         lib.sas_sparse_attention(self.shape, q, K, V, page_table, seqlens, idx, k, self.k_max, lam, log_g,
                                  out, self.workspace, self.ws_bytes)
         return out
+
+    def append_chunk(self, K_new, V_new, q_start, M, K, V, Kproj, page_table, seqlens):
+        """K_new, V_new [n_new][Hkv][d], tokens at any stride; Kproj (and M) may be None."""
+        n_new, stride = _tokens(K_new, self.shape.Hkv, self.shape.d, "K_new")
+        if _tokens(V_new, self.shape.Hkv, self.shape.d, "V_new") != (n_new, stride):
+            raise ValueError("K_new and V_new differ in tokens or stride")
+        lib.sas_append_chunk(self.shape, K_new, V_new, stride, q_start, n_new, M, K, V, Kproj, page_table, seqlens,
+                             self.workspace, self.ws_bytes)
+
+    def chunk(self, q, q_start, K, V, page_table, seqlens, window=0, sinks=0, out=None, lse=None):
+        """q [n_new][Hq][d], tokens at any stride.  Returns out (bf16) and lse (None unless given)."""
+        n_new, stride = _tokens(q, self.shape.Hq, self.shape.d, "q")
+        if n_new > self.chunk_max:
+            raise ValueError(f"{n_new} new tokens, more than the session's {self.chunk_max}")
+        if out is None:
+            out = torch.empty(n_new, self.shape.Hq, self.shape.d, dtype=torch.bfloat16, device=q.device)
+        lib.sas_chunk_attention(self.shape, q, stride, q_start, n_new, K, V, page_table, seqlens, window, sinks, out,
+                                lse, self.workspace, self.ws_bytes)
+        return out, lse
+
+    def window(self, q, K, V, page_table, seqlens, window, sinks=0, weights=None, out=None, lse=None):
+        out = self.out if out is None else out
+        lib.sas_window_decode(self.shape, q, K, V, page_table, seqlens, window, sinks, out, lse, weights,
+                              self.workspace, self.ws_bytes)
+        return out, lse
+
+    def evict(self, weights, keep, sinks, recent, K, V, Kproj, log_g, page_table, seqlens, idx=None, weights_out=None,
+              seqlens_out=None):
+        """In place by default: weights and seqlens are updated where they are."""
+        idx = self.idx if idx is None else idx
+        lib.sas_evict(self.shape, weights, keep, self.k_max, sinks, recent, K, V, Kproj, log_g, page_table, seqlens,
+                      idx, weights if weights_out is None else weights_out,
+                      seqlens if seqlens_out is None else seqlens_out, self.workspace, self.ws_bytes)
+        return idx
 
     def check(self):
         """(status, code, where) of the device-side checks since the last check (synchronises)."""
