@@ -128,6 +128,81 @@ def test_append_chunk_one_token_is_append_proj(cuda_lib):
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+# ------------------------------------------------------------------------------------ chunk attention
+CHUNKS = [
+    # B, Hq, Hkv, d, seqlens, new, paged, window, sinks, pad, fused
+    (1, 1, 1, 64, [1], [1], False, 0, 0, 0, False),
+    (1, 1, 1, 128, [130], [130], False, 0, 0, 0, False),
+    (3, 8, 2, 128, [70, 64, 1], [1, 0, 1], True, 0, 0, 2, True),
+    (2, 32, 8, 128, [1500, 333], [5, 5], True, 0, 0, 0, False),
+    (2, 8, 2, 64, [700, 129], [700, 65], False, 0, 0, 3, True),
+    (4, 6, 2, 128, [513, 64, 200, 5], [300, 64, 0, 5], True, 100, 4, 1, False),
+    (2, 10, 2, 64, [515, 260], [40, 260], True, 64, 70, 0, True),
+    (2, 20, 4, 128, [900, 77], [101, 77], False, 1, 0, 0, False),
+    (3, 16, 1, 128, [2100, 40, 1000], [30, 40, 9], True, 500, 130, 7, False),
+    (1, 128, 1, 64, [300], [9], True, 0, 3, 0, False),
+    (2, 24, 8, 128, [1000, 640], [600, 640], False, 1 << 30, 5, 0, True),
+    (1, 4, 4, 64, [5000], [1024], True, 0, 0, 0, False),
+    (1, 8, 2, 128, [9000], [260], False, 2000, 4, 0, False),
+]
+
+
+def check_chunk(p, q, out, lse, out0, new, window, sinks):
+    G, sigma, at = p.Hq // p.Hkv, p.d ** -0.5, 0
+    out, q = f64(out), f64(q)
+    lse = None if lse is None else f64(lse)
+    for b in range(p.B):
+        n, T = int(p.seqlens[b]), new[b]
+        for h in range(p.Hkv):
+            k, v = (rows(p, x, b, h, np.arange(n)) for x in (p.K, p.V))
+            for t in sorted(set(range(min(T, 40))) | set(range(0, T, 7)) | set(range(max(0, T - 40), T))):
+                pos = np.nonzero(C.visible(n - T + t, n, window, sinks))[0]
+                ro, rl, w, W, pv = errors_of(q[at + t, h * G:(h + 1) * G], k[pos], v[pos], sigma, p.d)
+                o = out[at + t, h * G:(h + 1) * G]
+                tol = (W + (len(pos) + 64) * 2 * U + BF) * pv + BF * np.abs(ro) + 1e-30
+                assert np.all(np.abs(o - ro) <= tol), (b, h, t, np.max(np.abs(o - ro) / tol))
+                if lse is not None:
+                    g = lse[at + t, h * G:(h + 1) * G]
+                    assert np.all(np.abs(g - rl) <= W[:, 0] + 2.0 ** -21 * (1 + np.abs(rl))), (b, h, t)
+        at += T
+    assert np.array_equal(out[at:], out0[at:])  # rows behind the last sequence stay as they were
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,d,seqlens,new,paged,window,sinks,pad,fused", CHUNKS)
+def test_chunk_attention(cuda_lib, B, Hq, Hkv, d, seqlens, new, paged, window, sinks, pad, fused):
+    p = problem(B, Hq, Hkv, d, seqlens, paged)
+    c = p.to("cuda")
+    for b in range(B):  # what no token of the chunk sees: pages given away, rows that are not finite
+        n, T = seqlens[b], new[b]
+        seen = np.zeros(n, bool)
+        for t in range(T):
+            seen |= C.visible(n - T + t, n, window, sinks)
+        if T == 0:
+            continue
+        for x in (c.K, c.V):
+            i1, i3 = C.slot(None if p.page_table is None else p.page_table.numpy(), b, np.nonzero(~seen)[0])
+            x[torch.from_numpy(i1).cuda(), :, torch.from_numpy(i3).cuda()] = float("nan")
+        if paged:
+            for lp in range((n + 63) // 64):
+                if not seen[lp * 64:lp * 64 + 64].any():
+                    c.page_table[b, lp] = -77
+    total = sum(new) + pad
+    g = torch.Generator().manual_seed(6)
+    buf = torch.randn(total, Hq * d + (24 if fused else 0), generator=g).to(torch.bfloat16)
+    buf[sum(new):] = float("nan")
+    q = buf[:, :Hq * d].unflatten(1, (Hq, d))
+    s = lib_and_session(c, chunk=total)
+    out = torch.full((total, Hq, d), 7.0, device="cuda", dtype=torch.bfloat16)
+    lse = torch.full((total, Hq), 7.0, device="cuda")
+    s.chunk(buf.cuda()[:, :Hq * d].unflatten(1, (Hq, d)), starts_of(new).cuda(), c.K, c.V, c.page_table, c.seqlens,
+            window, sinks, out=out, lse=lse)
+    assert s.check()[0] == 0
+    check_chunk(p, q, out, lse, np.full(out.shape, 7.0), new, window, sinks)
+    again, none = s.chunk(q.cuda(), starts_of(new).cuda(), c.K, c.V, c.page_table, c.seqlens, window, sinks)
+    assert none is None and torch.equal(again[:sum(new)], out[:sum(new)])
+
+
 # ------------------------------------------------------------------------------------ window decode
 WINDOWS = [
     # B, Hq, Hkv, d, seqlens, paged, window, sinks

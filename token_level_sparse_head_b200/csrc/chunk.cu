@@ -1,8 +1,787 @@
+// Causal attention of a chunk of new tokens over the cache, with a sliding window and sinks (sm_100a).
+//
+//   out[t] = sum_j softmax_j(sigma q_t . K_j) V_j over the j visible to token t.
+//
+// Rows: the G query heads of a KV head read the same K and V, so a 128-row tile holds 128 / G
+// tokens times G heads.  A task is up to two tiles of one sequence; its keys are a list of 64-row
+// pages (the sinks' pages, then those from the window of its first token to its last token).
+// Work: units of all tasks and KV heads, one after another, cut into equal contiguous shares, one
+// per CTA, so that ragged batches, causal triangles and few long sequences load every SM alike.
+//   two tiles  a unit is one block of 128 keys, read once for both tiles;
+//   one tile   a unit is two blocks; each warpgroup takes one, with its own statistics and output
+//              (drafted tokens and short chunks: the cache is read at twice the rate per step).
+// A share that holds part of a task leaves a partial (m, l, O); merge_kernel joins those in order.
+//
+// CTA: two softmax warpgroups (a thread is a row), one thread that issues the matrix
+// instructions, one warp that loads.  S = Q K^T goes to tensor memory; the softmax threads read
+// their row, write P in bf16 over it, and P V takes its left operand from there, so P never
+// passes through shared memory.  The two tiles alternate: while one is exponentiated, the
+// other's products run.  O is rescaled only when a row's maximum has grown by 2^8 since the last
+// time (P <= 2^8 keeps bf16's relative rounding and fp32's range), which after the first blocks is rare.
+// K and V blocks of 128 keys pass through one ring of tiled bulk copies (128-byte swizzle).
 #include "sas_device.cuh"
 #include "sas_kernels.h"
+
 namespace sas {
-void plan_chunk(ChunkParams& p) {}
-size_t chunk_workspace_bytes(const ChunkParams& p) { return 0; }
-void bind_chunk(ChunkParams& p, void* scratch) {}
-cudaError_t launch_chunk(const ChunkParams& p, cudaStream_t stream) { return cudaErrorNotSupported; }
+namespace {
+
+constexpr int kPage = 64;
+constexpr int kThreads = 384;      // 8 softmax warps, 1 matrix warp, 1 load warp, 2 idle: three warpgroups
+constexpr int kPlanThreads = 1024;
+constexpr int kTile = 128;
+constexpr int kMergeRows = 32;
+constexpr int kMergeThreads = 256;
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int D>
+struct Geo {
+  static constexpr int HALVES = D / 64;
+  static constexpr int HALF_BYTES = kTile * 128;           // 128 rows of 64 columns
+  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;   // Q tile, K block or V block
+  static constexpr int STAGES = D == 128 ? 5 : 8;
+  static constexpr int SMEM = 1024 + (2 + STAGES) * TILE_BYTES;
+  static constexpr int COL_O = 256;                        // S0, S1 at columns 0 and 128
+};
+
+// ----------------------------------------------------------------------------- tensor memory
+__device__ __forceinline__ void tmem_ld32(float* r, uint32_t addr) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(addr));
 }
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(u[0]),
+      "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+      "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
+      "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
+      "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// All matrix instructions this thread has issued so far arrive on `bar` when they are done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Shared-memory operand of 128-byte swizzled rows.  `lead` is the distance between 64-column
+// parts of a row-contiguous (MN-major) operand; consecutive groups of 8 rows lie 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// bf16 x bf16 -> fp32, 128 rows, n columns; b_rows: B is stored [k][n].
+constexpr uint32_t mma_form(int n, bool b_rows) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_rows ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t form, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(form), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t form, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(form), "r"((uint32_t)add)
+      : "memory");
+}
+
+// ----------------------------------------------------------------------------- waits
+// Waits for a phase; gives up when another warp has or after a few seconds' worth of cycles.
+constexpr long long kWaitCycles = 4000000000LL;
+__device__ __forceinline__ bool wait_live(uint64_t* bar, uint32_t parity, volatile int* stop) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*stop) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *stop = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The softmax threads hold a row of 128 scores; the launch's 384 x 168 registers are dealt out
+// again as 2 x 128 x 208 + 128 x 88.
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+// Bits 0 .. x-1 of a 64-row page.
+__device__ __forceinline__ uint64_t low_bits(int x) { return x <= 0 ? 0ull : (x >= 64 ? ~0ull : (1ull << x) - 1); }
+
+// ----------------------------------------------------------------------------- plan
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {  // inclusive, kPlanThreads threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  T before = 0;
+  total = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  __syncthreads();
+  return x + before;
+}
+
+// Tasks of every sequence, and the units before each: tasks[slots] holds their number and total.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ int off_s[kPlanThreads + 1], sum_s[kPlanThreads / 32];
+  __shared__ long long lsum_s[kPlanThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int span = 2 * p.tok_tile;
+  int base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int cnt = 0;
+    if (b < p.B) {
+      const int s0 = p.q_start[b], s1 = p.q_start[b + 1], n = p.seqlens[b];
+      if (n < 0 || n > p.cap) record_error(p.err, kDevBadSeqlen, (uint32_t)b);
+      else if (s0 < 0 || s1 < s0 || s1 > p.n_new || s1 - s0 > n) record_error(p.err, kDevBadChunk, (uint32_t)b);
+      else cnt = (s1 - s0 + span - 1) / span;
+    }
+    int total;
+    int end = block_scan(cnt, sum_s, total);
+    // sequences that overlap could exceed the slots: such a sequence is skipped
+    if (base + end > p.slots && cnt > 0) {
+      record_error(p.err, kDevBadChunk, (uint32_t)b);
+      end = p.slots - base;
+    }
+    if (tid == 0) off_s[0] = 0;
+    off_s[tid + 1] = min(end, p.slots - base);
+    __syncthreads();
+    for (int i = warp; i < min(kPlanThreads, p.B - b0); i += kPlanThreads / 32) {
+      const int k0 = off_s[i], k1 = off_s[i + 1];
+      if (k0 >= k1) continue;
+      const int s0 = p.q_start[b0 + i], T = p.q_start[b0 + i + 1] - s0, n = p.seqlens[b0 + i];
+      for (int k = k0 + lane; k < k1; k += 32) {
+        const int at = (k - k0) * span;
+        ChunkTask t;
+        t.b = b0 + i;
+        t.tok0 = s0 + at;
+        t.ntok = min(span, T - at);
+        t.pos0 = n - T + at;
+        t.unit0 = 0;
+        const int nv = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks).nv;
+        t.blocks = t.ntok > p.tok_tile ? (nv + 1) >> 1 : (nv + 3) >> 2;
+        t.seqlen = n;
+        p.tasks[base + k] = t;
+      }
+    }
+    __syncthreads();
+    base = min(base + total, p.slots);
+  }
+  long long units = 0;
+  for (int k0 = 0; k0 < base; k0 += kPlanThreads) {
+    const int k = k0 + tid;
+    const long long x = k < base ? p.tasks[k].blocks : 0;
+    long long total;
+    const long long end = block_scan(x, lsum_s, total);
+    if (k < base) p.tasks[k].unit0 = units + end - x;
+    units += total;
+  }
+  if (tid == 0) {
+    ChunkTask t = {};
+    t.b = base;
+    t.unit0 = units;
+    p.tasks[p.slots] = t;
+  }
+}
+
+// ----------------------------------------------------------------------------- shares
+struct Place {
+  int task, h, block;
+};
+// Task, KV head and unit of the task at global unit u; whole warp.
+__device__ __forceinline__ Place find_unit(const ChunkParams& p, long long u, int tasks, long long units) {
+  const int lane = threadIdx.x & 31;
+  Place c;
+  c.h = (int)(u / units);
+  const long long rem = u - c.h * units;
+  int lo = 0, cnt = tasks;
+  while (cnt > 1) {
+    const int step = (cnt + 31) / 32;
+    const bool in = lane * step < cnt && p.tasks[lo + lane * step].unit0 <= rem;
+    const int k = __popc(__ballot_sync(0xffffffffu, in)) - 1;
+    lo += k * step;
+    cnt = min(step, cnt - k * step);
+  }
+  c.task = lo;
+  c.block = (int)(rem - p.tasks[lo].unit0);
+  return c;
+}
+__device__ __forceinline__ void next_task(Place& c, int tasks) {
+  c.block = 0;
+  if (++c.task == tasks) {
+    c.task = 0;
+    ++c.h;
+  }
+}
+
+// Ring positions of the blocks of a segment of n units, counted from its first.  Two tiles: K0 V0
+// K1 V1 ...; one tile: K0 K1, then V(2j) K(2j+2) V(2j+1) K(2j+3) for unit j: the order of use.
+__device__ __forceinline__ int ring_k(bool one, int j, int t) { return !one ? 2 * j : (j == 0 ? t : 4 * j - 1 + 2 * t); }
+__device__ __forceinline__ int ring_v(bool one, int j, int t, int n) {
+  return !one ? 2 * j + 1 : 4 * j + 2 + (j + 1 < n ? 2 * t : t);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+  using Gm = Geo<D>;
+  constexpr int ST = Gm::STAGES;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* ring = qs + 2 * Gm::TILE_BYTES;
+  __shared__ uint64_t full[ST], empty[ST], q_full, q_empty, s_full[2], p_ready[2], o_full[2], half_full, half_free, drain;
+  __shared__ uint32_t tmem_s;
+  __shared__ volatile int stop_s;
+  __shared__ Place start_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_ready[t], 4);
+      mbar_init(&o_full[t], 1);
+    }
+    mbar_init(&half_full, 4);
+    mbar_init(&half_free, 4);
+    mbar_init(&drain, 1);
+    fence_barrier_init();
+    stop_s = 0;
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_s)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  pdl_trigger();
+  const int tasks = p.tasks[p.slots].b;
+  const long long units = p.tasks[p.slots].unit0;
+  const long long total = units * p.Hkv, share = (total + p.ctas - 1) / p.ctas;
+  const long long u0 = min(share * blockIdx.x, total), u1 = min(u0 + share, total);
+  if (warp == 0 && u0 < u1) {
+    const Place c = find_unit(p, u0, tasks, units);
+    if (lane == 0) start_s = c;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  Place c = start_s;
+
+  if (warp >= 8) regs_down();
+  if (warp == 9) {
+    // ---------------------------------------------------------------- loads
+    int cnt = 0, seg = 0;  // blocks and Q tiles asked for
+    bool live = true;
+    for (long long u = u0; u < u1 && live;) {
+      const ChunkTask t = p.tasks[c.task];
+      const int be = (int)min((long long)t.blocks, c.block + (u1 - u)), units_here = be - c.block;
+      const bool one = t.ntok <= p.tok_tile;
+      const VisiblePages vis = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks);
+      if (lane == 0) {
+        live = seg == 0 || wait_live(&q_empty, (seg - 1) & 1, &stop_s);
+        if (live) {
+          const int box = p.G * p.tok_tile * 128;
+          mbar_arrive_expect_tx(&q_full, (one ? 1 : 2) * Gm::HALVES * box);
+          for (int i = 0; i < (one ? 1 : 2); ++i)
+#pragma unroll
+            for (int hf = 0; hf < Gm::HALVES; ++hf)
+              tma_3d(qs + i * Gm::TILE_BYTES + hf * Gm::HALF_BYTES, &p.qmap, hf * 64, c.h * p.G, t.tok0 + i * p.tok_tile, &q_full);
+        }
+      }
+      live = __shfl_sync(0xffffffffu, live, 0);
+      if (live) ++seg;
+      // rows of 32 pages, page v with lane v % 32, looked up 16 at a time
+      int row = 0, have = c.block * (one ? 4 : 2);
+      auto push = [&](const CUtensorMap* map, int v) {
+        while (v + 2 > have) {
+          const int w = have + ((lane - have) & 31);
+          if (w < have + 16) {
+            row = p.row_end;
+            const int lp = vis.page(w);
+            if (w < vis.nv) {
+              if (p.paged) {
+                const int pg = p.page_table[(size_t)t.b * p.max_pages + lp];
+                if (pg < 0 || pg >= p.num_pages) record_error(p.err, kDevBadPage, (uint32_t)t.b);
+                else row = (pg * p.Hkv + c.h) * kPage;
+              } else {
+                row = (t.b * p.Hkv + c.h) * p.cap + lp * kPage;
+              }
+            }
+          }
+          have += 16;
+        }
+        const int y0 = __shfl_sync(0xffffffffu, row, v & 31), y1 = __shfl_sync(0xffffffffu, row, (v + 1) & 31);
+        if (lane == 0 && live) {
+          const int st = cnt % ST;
+          live = cnt < ST || wait_live(&empty[st], ((cnt / ST) & 1) ^ 1, &stop_s);
+          if (live) {
+            unsigned char* dst = ring + (size_t)st * Gm::TILE_BYTES;
+            mbar_arrive_expect_tx(&full[st], Gm::TILE_BYTES);
+#pragma unroll
+            for (int hf = 0; hf < Gm::HALVES; ++hf) {
+              tma_2d(dst + hf * Gm::HALF_BYTES, map, hf * 64, y0, &full[st]);
+              tma_2d(dst + hf * Gm::HALF_BYTES + kPage * 128, map, hf * 64, y1, &full[st]);
+            }
+          }
+        }
+        live = __shfl_sync(0xffffffffu, live, 0);
+        if (live) ++cnt;
+      };
+      if (one) {
+        push(&p.kmap, 4 * c.block);
+        push(&p.kmap, 4 * c.block + 2);
+        for (int j = c.block; j < be; ++j)
+          for (int x = 0; x < 2; ++x) {
+            push(&p.vmap, 4 * j + 2 * x);
+            if (j + 1 < be) push(&p.kmap, 4 * j + 4 + 2 * x);
+          }
+      } else {
+        for (int j = c.block; j < be; ++j) {
+          push(&p.kmap, 2 * j);
+          push(&p.vmap, 2 * j);
+        }
+      }
+      u += units_here;
+      next_task(c, tasks);
+    }
+    // after a wait that ran out: the copies in flight land before the CTA ends
+    if (lane == 0 && !live) {
+      if (seg > 0) mbar_wait_bounded(&q_full, (seg - 1) & 1);
+      for (int i = max(0, cnt - ST); i < cnt; ++i) mbar_wait_bounded(&full[i % ST], (i / ST) & 1);
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- matrix instructions
+    if (lane == 0) {
+      constexpr uint32_t kFormS = mma_form(kTile, false), kFormO = mma_form(D, true);
+      const uint32_t qb = smem_u32(qs), rb = smem_u32(ring);
+      int base = 0, seg = 0;
+      uint32_t ph_p[2] = {0, 0};
+      bool live = true;
+      auto stage = [&](int idx) { return idx % ST; };
+      auto scores = [&](int x, bool one, int idx) {  // S_x = Q K^T
+        const int st = stage(idx);
+        live = live && wait_live(&full[st], (idx / ST) & 1, &stop_s);
+        if (!live) return;
+        tc_fence_after();
+        const uint32_t a = qb + (one ? 0 : x) * Gm::TILE_BYTES, b = rb + st * Gm::TILE_BYTES;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (k >> 2) * Gm::HALF_BYTES + (k & 3) * 32;
+          mma_ss(tmem + x * kTile, operand(a + o, 16), operand(b + o, 16), kFormS, k > 0);
+        }
+        tc_commit(&s_full[x]);
+        if (one || x == 1) tc_commit(&empty[st]);
+      };
+      for (long long u = u0; u < u1 && live; ++seg) {
+        const ChunkTask t = p.tasks[c.task];
+        const int n = (int)min((long long)t.blocks - c.block, u1 - u);
+        const bool one = t.ntok <= p.tok_tile;
+        live = wait_live(&q_full, seg & 1, &stop_s);
+        scores(0, one, base + ring_k(one, 0, 0));
+        scores(1, one, base + ring_k(one, 0, 1));
+        if (n == 1 && live) tc_commit(&q_empty);
+        for (int j = 0; j < n && live; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            live = live && wait_live(&p_ready[x], ph_p[x], &stop_s);
+            ph_p[x] ^= 1;
+            const int idx = base + ring_v(one, j, x, n), st = stage(idx);
+            live = live && wait_live(&full[st], (idx / ST) & 1, &stop_s);
+            if (!live) break;
+            tc_fence_after();
+            const uint32_t b = rb + st * Gm::TILE_BYTES;
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_ts(tmem + Gm::COL_O + x * D, tmem + x * kTile + k * 8, operand(b + k * 2048, Gm::HALF_BYTES), kFormO, j > 0 || k > 0);
+            if (one || x == 1) tc_commit(&empty[st]);
+            if (j + 1 < n) {
+              scores(x, one, base + ring_k(one, j + 1, x));
+              if (j + 2 == n && x == 1 && live) tc_commit(&q_empty);
+            } else {
+              tc_commit(&o_full[x]);
+            }
+          }
+        base += (one ? 4 : 2) * n;
+        u += n;
+        next_task(c, tasks);
+      }
+      // every product has left shared and tensor memory before they are given back
+      tc_commit(&drain);
+      mbar_wait_bounded(&drain, 0);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- softmax and output
+    regs_up();
+    const int x = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + x * kTile + lanes, tO = tmem + Gm::COL_O + x * D + lanes;
+    const float scale = p.scale_log2, grow_by = 8.f / scale;
+    int base = 0;
+    uint32_t ph_s = 0, ph_o = 0, ph_half = 0;
+    bool live = true, half_used = false;
+    for (long long u = u0; u < u1 && live;) {
+      const ChunkTask t = p.tasks[c.task];
+      const int n_seq = t.seqlen;
+      const int n = (int)min((long long)t.blocks - c.block, u1 - u);
+      const bool one = t.ntok <= p.tok_tile;
+      const VisiblePages vis = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks);
+      const int tile = one ? 0 : x;
+      const int toks = min(p.tok_tile, t.ntok - tile * p.tok_tile);
+      const int plo = t.pos0 + tile * p.tok_tile, phi = plo + toks - 1;
+      const bool mine = r < toks * p.G, busy = quad * 32 < toks * p.G;
+      const int tok = r / p.G, pos = plo + tok;
+      const int wlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;  // first of the row's window
+      float m = -INFINITY, l = 0.f;
+
+      for (int j = 0; j < n; ++j) {
+        const int v0 = one ? (c.block + j) * 4 + 2 * x : (c.block + j) * 2;
+        live = __all_sync(0xffffffffu, wait_live(&s_full[x], ph_s, &stop_s));
+        ph_s ^= 1;
+        if (!live) break;
+        tc_fence_after();
+        bool whole = true, dirty = false;
+        int at[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j0 = vis.page(v0 + i) * kPage;
+          at[i] = v0 + i < vis.nv ? j0 : -1;
+          if (v0 + i >= vis.nv) {
+            whole = false;
+          } else {
+            whole = whole && j0 + kPage - 1 <= plo &&
+                    (p.window <= 0 || j0 > phi - p.window || j0 + kPage <= p.sinks);
+            // rows that no token sees may hold anything, and 0 * NaN is not 0
+            dirty = dirty || j0 + kPage > n_seq || (j0 < vis.first && j0 + kPage > p.sinks);
+          }
+        }
+        if (dirty) {
+          const int idx = base + ring_v(one, j, x, n), st = idx % ST;
+          live = __all_sync(0xffffffffu, wait_live(&full[st], (idx / ST) & 1, &stop_s));
+          if (!live) break;
+          const int a = r < 64 ? at[0] : at[1], pj = a + (r & 63);
+          if (a >= 0 && (pj >= n_seq || (pj < vis.first && pj >= p.sinks))) {
+            unsigned char* z = ring + (size_t)st * Gm::TILE_BYTES + r * 128;
+#pragma unroll
+            for (int hf = 0; hf < Gm::HALVES; ++hf)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(z + hf * Gm::HALF_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (busy) {
+          float s[kTile];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s + 32 * i, tS + 32 * i);
+          tmem_wait_ld();
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint64_t see = 0;
+              if (mine && at[i] >= 0)
+                see = low_bits(pos + 1 - at[i]) & (~low_bits(wlo - at[i]) | low_bits(p.sinks - at[i]));
+              const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                if (!((lo >> e) & 1)) s[64 * i + e] = -INFINITY;
+                if (!((hi >> e) & 1)) s[64 * i + 32 + e] = -INFINITY;
+              }
+            }
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 4; i < kTile - 4; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kTile - 4 + e]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (__any_sync(0xffffffffu, mine && top > m + grow_by)) {
+            const float mn = fmaxf(m, top);
+            if (j > 0) {
+              // S(j) is complete, so P V of block j - 1, issued before it, is too
+              const float f = m == -INFINITY ? 0.f : ex2((m - mn) * scale);
+              l *= f;
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) {
+                float o[32];
+                tmem_ld32(o, tO + 32 * i);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= f;
+                tmem_st32(tO + 32 * i, reinterpret_cast<const uint32_t*>(o));
+              }
+            }
+            m = mn;
+          }
+          const float off = m == -INFINITY ? 0.f : -m * scale;
+          const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float2 z = ffma2(make_float2(s[64 * i + 2 * e], s[64 * i + 2 * e + 1]), sc2, off2);
+              z.x = ex2(z.x);
+              z.y = ex2(z.y);
+              sum[e & 1] = __fadd2_rn(sum[e & 1], z);
+              w[e] = pack_bf16(z.x, z.y);
+            }
+            tmem_st32(tS + 32 * i, w);
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[x]);
+      }
+      if (!live) break;
+
+      // ---- this segment's rows ----
+      live = __all_sync(0xffffffffu, wait_live(&o_full[x], ph_o, &stop_s));
+      ph_o ^= 1;
+      if (!live) break;
+      tc_fence_after();
+      const bool done = n == t.blocks;
+      const int slot = 2 * (int)blockIdx.x + (u == u0 ? 0 : 1);
+      float4* part = reinterpret_cast<float4*>(p.part) + (size_t)slot * (D / 4) * p.rows_cap;
+      float2* ml = p.ml + (size_t)slot * p.rows_cap;
+      const float mz = m == -INFINITY ? m : m * scale;
+      if (!done || (one && x == 1)) {
+        if (done && half_used) {  // the other warpgroup has read the half it got before
+          live = __all_sync(0xffffffffu, wait_live(&half_free, ph_half ^ 1, &stop_s));
+          if (!live) break;
+        }
+        if (busy) {
+          const int at = x * kTile + r;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            float o[32];
+            tmem_ld32(o, tO + 32 * i);
+            tmem_wait_ld();
+            if (mine)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                part[(size_t)(8 * i + e) * p.rows_cap + at] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          if (mine) ml[at] = make_float2(mz, l);
+        }
+        if (done) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&half_full);
+          half_used = true;
+          ph_half ^= 1;
+        }
+      } else {
+        float f0 = 1.f, f1 = 0.f, M = mz, L = l;
+        if (one) {
+          live = __all_sync(0xffffffffu, wait_live(&half_full, ph_half, &stop_s));
+          ph_half ^= 1;
+          if (!live) break;
+          if (mine) {
+            const float2 y = __ldcg(ml + kTile + r);
+            M = fmaxf(mz, y.x);
+            f0 = mz == -INFINITY ? 0.f : ex2(mz - M);
+            f1 = y.x == -INFINITY ? 0.f : ex2(y.x - M);
+            L = l * f0 + y.y * f1;
+          }
+        }
+        if (busy) {
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const size_t o_row = (size_t)(t.tok0 + tile * p.tok_tile + tok) * p.Hq + c.h * p.G + r % p.G;
+          uint4* dst = reinterpret_cast<uint4*>(p.out + o_row * D);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            float o[32];
+            tmem_ld32(o, tO + 32 * i);
+            tmem_wait_ld();
+            if (!mine) continue;
+            if (one) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 y = __ldcg(part + (size_t)(8 * i + e) * p.rows_cap + kTile + r);
+                o[4 * e] = o[4 * e] * f0 + y.x * f1;
+                o[4 * e + 1] = o[4 * e + 1] * f0 + y.y * f1;
+                o[4 * e + 2] = o[4 * e + 2] * f0 + y.z * f1;
+                o[4 * e + 3] = o[4 * e + 3] * f0 + y.w * f1;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[4 * i + e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                          pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          }
+          if (mine && p.lse != nullptr) p.lse[o_row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+        }
+        if (one) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&half_free);
+        }
+      }
+      base += (one ? 4 : 2) * n;
+      u += n;
+      next_task(c, tasks);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (tid == 0 && stop_s) record_error(p.err, kDevWaitTimeout, blockIdx.x);
+}
+
+// Joins the partials of a task that several CTAs share, in CTA order.  blockIdx.x + 1 is the
+// share whose beginning is looked at: the first one inside a task acts for it, 32 rows a CTA.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ Place at_s;
+  pdl_wait();
+  pdl_trigger();
+  const int tasks = p.tasks[p.slots].b;
+  const long long units = p.tasks[p.slots].unit0;
+  const long long total = units * p.Hkv, share = (total + p.ctas - 1) / p.ctas;
+  const long long u = share * (blockIdx.x + 1);
+  if (u >= total) return;
+  if (threadIdx.x < 32) {
+    const Place c = find_unit(p, u, tasks, units);
+    if (threadIdx.x == 0) at_s = c;
+  }
+  __syncthreads();
+  const Place c = at_s;
+  if (c.block == 0) return;
+  const ChunkTask t = p.tasks[c.task];
+  const long long t0 = u - c.block;                      // the task's first unit
+  const int c0 = (int)(t0 / share), c1 = (int)((t0 + t.blocks - 1) / share);
+  if (c0 != (int)blockIdx.x) return;
+  const bool one = t.ntok <= p.tok_tile;
+  const int np = (c1 - c0 + 1) * (one ? 2 : 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.y * kMergeRows + lane;        // row of the task's 256
+  const int tile = row / kTile, r = row % kTile;
+  const int toks = min(p.tok_tile, t.ntok - tile * p.tok_tile);
+  if (r >= toks * p.G) return;
+  // partial i: slot of its CTA, and its row there
+  auto slot = [&](int i) {
+    const int k = one ? i >> 1 : i;
+    return k == 0 ? 2 * c0 + (t0 == c0 * share ? 0 : 1) : 2 * (c0 + k);
+  };
+  auto srow = [&](int i) { return one ? r + kTile * (i & 1) : row; };
+  float M = -INFINITY, L = 0.f;
+  for (int i = 0; i < np; ++i) M = fmaxf(M, p.ml[(size_t)slot(i) * p.rows_cap + srow(i)].x);
+  constexpr int C4 = D / 4 / (kMergeThreads / 32);       // float4 columns per thread
+  float4 acc[C4];
+#pragma unroll
+  for (int e = 0; e < C4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = 0; i < np; ++i) {
+    const float2 y = p.ml[(size_t)slot(i) * p.rows_cap + srow(i)];
+    const float f = y.x == -INFINITY ? 0.f : ex2(y.x - M);
+    L += f * y.y;
+    const float4* part = reinterpret_cast<const float4*>(p.part) + (size_t)slot(i) * (D / 4) * p.rows_cap + srow(i);
+#pragma unroll
+    for (int e = 0; e < C4; ++e) {
+      const float4 o = __ldcg(part + (size_t)(warp * C4 + e) * p.rows_cap);
+      acc[e].x += f * o.x;
+      acc[e].y += f * o.y;
+      acc[e].z += f * o.z;
+      acc[e].w += f * o.w;
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const size_t o_row = (size_t)(t.tok0 + tile * p.tok_tile + r / p.G) * p.Hq + c.h * p.G + r % p.G;
+  uint4* dst = reinterpret_cast<uint4*>(p.out + o_row * D + warp * C4 * 4);
+#pragma unroll
+  for (int e = 0; e < C4; e += 2)
+    dst[e / 2] = make_uint4(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv),
+                            pack_bf16(acc[e + 1].x * inv, acc[e + 1].y * inv), pack_bf16(acc[e + 1].z * inv, acc[e + 1].w * inv));
+  if (warp == 0 && p.lse != nullptr) p.lse[o_row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int D>
+cudaError_t launch_d(const ChunkParams& p, cudaStream_t stream) {
+  cudaError_t e = prepare_kernel((const void*)chunk_kernel<D>, Geo<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(chunk_kernel<D>, dim3((unsigned)p.ctas), dim3(kThreads), (size_t)Geo<D>::SMEM, stream, p);
+  if (e != cudaSuccess || p.ctas == 1) return e;
+  const int rows = p.n_new > p.tok_tile ? 2 * kTile : kTile;
+  return launch_pdl(merge_kernel<D>, dim3((unsigned)(p.ctas - 1), (unsigned)(rows / kMergeRows)), dim3(kMergeThreads), 0, stream, p);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+void plan_chunk(ChunkParams& p) {
+  p.tok_tile = kTile / p.G;
+  p.slots = p.n_new / (2 * p.tok_tile) + p.B;
+  p.rows_cap = 2 * kTile;
+}
+
+size_t chunk_workspace_bytes(const ChunkParams& p) {
+  return up256((size_t)(p.slots + 1) * sizeof(ChunkTask)) +
+         (size_t)2 * kChunkMaxCtas * p.rows_cap * (sizeof(float2) + (size_t)p.d * 4);
+}
+
+void bind_chunk(ChunkParams& p, void* scratch) {
+  unsigned char* w = static_cast<unsigned char*>(scratch);
+  p.tasks = reinterpret_cast<ChunkTask*>(w);
+  w += up256((size_t)(p.slots + 1) * sizeof(ChunkTask));
+  p.ml = reinterpret_cast<float2*>(w);
+  w += (size_t)2 * kChunkMaxCtas * p.rows_cap * sizeof(float2);
+  p.part = reinterpret_cast<float*>(w);
+}
+
+cudaError_t launch_chunk(const ChunkParams& p, cudaStream_t stream) {
+  if (p.d == 128) return launch_d<128>(p, stream);
+  if (p.d == 64) return launch_d<64>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace sas

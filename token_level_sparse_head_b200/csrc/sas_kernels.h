@@ -142,7 +142,7 @@ cudaError_t launch_append_chunk(const AppendParams& p, int num_sms, cudaStream_t
 struct ChunkTask {
   int32_t b, tok0, ntok, pos0;  // sequence, first row of q, tokens, position of the first
   long long unit0;              // units of the tasks before this one (one KV head)
-  int32_t blocks, pad;
+  int32_t blocks, seqlen;     // units of this task, cached tokens of the sequence
 };
 struct ChunkParams {
   CUtensorMap qmap, kmap, vmap;
