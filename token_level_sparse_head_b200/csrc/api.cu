@@ -679,6 +679,17 @@ sas::WindowParams window_plan(const sas_shape* s, int32_t window, int32_t sinks)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// No more rows than the capacity are kept.
+int evict_segments(const sas_shape* s, int32_t keep_max) {
+  const int most = keep_max < cap_of(s) ? keep_max : cap_of(s);
+  return most > 0 ? (most + 63) / 64 : 1;
+}
+// Plan, ticket and flags of an eviction, before its keys.
+size_t evict_head_bytes(const sas_shape* s, int32_t keep_max) {
+  const size_t n = (size_t)s->B * sizeof(int2) + 16 + (size_t)s->B * s->Hkv * evict_segments(s, keep_max) * 4;
+  return (n + 255) & ~(size_t)255;
+}
+
 }  // namespace
 
 extern "C" {
@@ -804,8 +815,7 @@ sas_status sas_window_decode(const sas_shape* shape, const void* q, const void* 
 
 size_t sas_evict_workspace_bytes(const sas_shape* shape, int32_t keep_max) {
   if (check_shape(shape) != SAS_OK || keep_max < 1) return 0;
-  return scratch_offset(shape) + (((size_t)shape->B * sizeof(int2) + 255) & ~(size_t)255) +
-         (size_t)shape->B * shape->Hkv * cap_of(shape) * 4;
+  return scratch_offset(shape) + evict_head_bytes(shape, keep_max) + (size_t)shape->B * shape->Hkv * cap_of(shape) * 4;
 }
 
 sas_status sas_evict(const sas_shape* shape, const float* weights, const int32_t* keep, int32_t keep_max,
@@ -843,7 +853,10 @@ sas_status sas_evict(const sas_shape* shape, const float* weights, const int32_t
   p.err = reinterpret_cast<uint32_t*>(w);
   p.hist = reinterpret_cast<uint32_t*>(w + kErrBytes);
   p.plan = reinterpret_cast<int2*>(scratch);
-  p.keys = reinterpret_cast<uint32_t*>(scratch + (((size_t)shape->B * sizeof(int2) + 255) & ~(size_t)255));
+  p.ticket = reinterpret_cast<uint32_t*>(scratch + (size_t)shape->B * sizeof(int2));
+  p.flags = p.ticket + 4;
+  p.segs = evict_segments(shape, keep_max);
+  p.keys = reinterpret_cast<uint32_t*>(scratch + evict_head_bytes(shape, keep_max));
   p.B = shape->B; p.Hkv = shape->Hkv; p.cap = cap_of(shape);
   p.max_pages = shape->max_pages; p.num_pages = shape->num_pages; p.paged = shape->page_size ? 1 : 0;
   p.keep_max = keep_max; p.sinks = sinks; p.recent = recent;
@@ -860,7 +873,7 @@ sas_status sas_evict(const sas_shape* shape, const float* weights, const int32_t
   sl.B = shape->B; sl.Hkv = shape->Hkv; sl.cap = p.cap; sl.k_max = keep_max;
   if (!sas::plan_select(sl, num_sms())) return fail(SAS_ERR_UNSUPPORTED, "no selection plan for this shape");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = sas::launch_evict_keys(p, st);
+  cudaError_t e = sas::launch_evict_keys(p, num_sms(), st);
   if (e != cudaSuccess) return cuda_fail(e, "eviction keys launch");
   e = sas::launch_select(sl, st);
   if (e != cudaSuccess) return cuda_fail(e, "select kernel launch");

@@ -214,11 +214,15 @@ struct EvictParams {
   uint32_t* keys;              // workspace: [B][Hkv][cap]
   uint32_t* hist;              // workspace: [B][Hkv][kHistBins]
   int2* plan;                  // workspace: [B] (N_b, rows kept)
+  uint32_t* ticket;            // workspace: segments handed out
+  uint32_t* flags;             // workspace: [B][Hkv][segs] whether a segment's sources have been read
+  int keys_per_cta;
+  int segs;                    // segments of 64 kept rows of a (b, h), at least 1
   uint32_t* err;
   int B, Hkv, cap, max_pages, num_pages, paged, keep_max, sinks, recent;
   int row_bytes, proj_bytes;   // bytes of a K row and of a projected row
 };
-cudaError_t launch_evict_keys(const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_evict_keys(EvictParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t stream);
 
 // 2D map of bf16 rows [rows][d] read in boxes of 64 columns (128 swizzled bytes) by box_rows rows.
