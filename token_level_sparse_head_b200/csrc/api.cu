@@ -796,6 +796,7 @@ sas_status sas_window_decode(const sas_shape* shape, const void* q, const void* 
   sas::WindowParams p = window_plan(shape, window, sinks);
   unsigned char* w = static_cast<unsigned char*>(workspace);
   sas::bind_window(p, w + scratch_offset(shape), weights != nullptr);
+  p.arrived = reinterpret_cast<uint32_t*>(w + kErrBytes);  // the histograms' place, at least 8192 zeros
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.page_table = shape->page_size ? page_table : nullptr;
   p.seqlens = seqlens;

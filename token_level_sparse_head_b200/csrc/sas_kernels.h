@@ -170,9 +170,6 @@ void bind_chunk(ChunkParams& p, void* scratch);
 cudaError_t launch_chunk(const ChunkParams& p, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------- window decode
-struct WindowDesc {            // where a CTA's share of the pages begins
-  int32_t b, h, hg, page, nv, pad[3];
-};
 struct WindowParams {
   CUtensorMap kmap, vmap;
   const __nv_bfloat16* q;      // [B][Hq][d]
@@ -182,7 +179,7 @@ struct WindowParams {
   float* lse;                  // [B][Hq] or null
   float* weights;              // [B][Hkv][cap] or null
   uint32_t* err;
-  WindowDesc* desc;            // workspace: [ctas + 1] (the last: total pages in page, share in nv)
+  uint32_t* arrived;           // workspace, zero between calls: partials left, by the task's first CTA
   float* part;                 // workspace: [2 * ctas][16][d]
   float2* ml;                  // workspace: [2 * ctas][16]
   float* lse2;                 // workspace: [B][Hq] base-2 log of the sums (with weights)

@@ -7,7 +7,7 @@
 // byte).  Work: the visible rows of a (b, h, group of up to 16 query heads) are a list of 64-row
 // pages (the sinks' pages, then the window's); the pages of all of them, one after another, are
 // cut into equal contiguous shares, one per CTA, so a ragged batch loads every SM alike.  A share
-// that holds part of a task leaves a partial (m, l, acc) and merge_kernel joins those in order.
+// that holds part of a task leaves a partial (m, l, acc); the last CTA of a task joins them in order.
 // CTA: one producer warp feeds a ring of pages with tiled bulk copies (128-byte swizzle); two
 // groups of four warps take the pages in turn, 16 rows of a page per warp.  The products run on
 // the warp-level matrix instruction with the heads as its 8 columns: 16 rows x 8 heads per
@@ -36,6 +36,7 @@ struct Geo {
   static constexpr int STAGES = D == 64 ? 8 : (NT == 1 ? 6 : 4);
   static constexpr int PITCH = D + 4;                     // floats: heads of a warp's merge rows
   static constexpr int MERGE = kConsumers * NT * 8 * PITCH;
+  static_assert(MERGE >= kChunkMaxCtas * 16, "the weights of the partials lie in the merge rows");
   static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + MERGE * 4;
 };
 
@@ -84,6 +85,52 @@ struct Cursor {
   int b, h, hg, page;
 };
 
+// Joins np partials of CTAs c0, c0 + 1, ...; the first is c0's second one if `second`.  All consumer threads.
+template <int D>
+__device__ void join_partials(const WindowParams& p, float (*wts)[16], float* inv_s, int np, int c0, bool second, int heads,
+                              size_t o0) {
+  auto slot = [&](int i) { return i == 0 ? 2 * (size_t)c0 + (second ? 1 : 0) : 2 * (size_t)(c0 + i); };
+  // 16 lanes of a half warp share a head
+  const int hd = threadIdx.x / 16, sub = threadIdx.x % 16;
+  float M = -INFINITY, L = 0.f;
+  if (hd < heads)
+    for (int i = sub; i < np; i += 16) M = fmaxf(M, __ldcg(&p.ml[slot(i) * 16 + hd]).x);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (hd < heads)
+    for (int i = sub; i < np; i += 16) {
+      const float2 x = __ldcg(&p.ml[slot(i) * 16 + hd]);
+      const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+      wts[i][hd] = f;
+      L += f * x.y;
+    }
+#pragma unroll
+  for (int o = 8; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (sub == 0 && hd < heads) {
+    inv_s[hd] = L > 0.f ? 1.f / L : 0.f;
+    const float ls = L > 0.f ? M + log2f(L) : -INFINITY;
+    if (p.lse != nullptr) p.lse[o0 + hd] = ls * 0.69314718055994531f;
+    if (p.lse2 != nullptr) p.lse2[o0 + hd] = ls;
+  }
+  consumers_sync();
+  for (int e = threadIdx.x; e < heads * (D / 4); e += kConsumers * 32) {
+    const int g = e / (D / 4), c4 = (e % (D / 4)) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < np; ++i) {
+      const float f = wts[i][g];
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + (slot(i) * 16 + g) * D + c4));
+      x.x += f * y.x;
+      x.y += f * y.y;
+      x.z += f * y.z;
+      x.w += f * y.w;
+    }
+    const float r = inv_s[g];
+    *reinterpret_cast<float4*>(p.out + (o0 + g) * D + c4) = make_float4(x.x * r, x.y * r, x.z * r, x.w * r);
+  }
+  consumers_sync();
+}
+
 template <int D, int NT, bool WEIGHTS>
 __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_constant__ WindowParams p) {
   using Gm = Geo<D, NT>;
@@ -94,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   __shared__ float wm[kConsumers][NT * 8], wl[kConsumers][NT * 8];
   __shared__ int red[kThreads / 32];
   __shared__ Cursor start_s;
+  __shared__ float inv_s[16];
+  __shared__ int last_s;
   __shared__ volatile int abort_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -128,7 +177,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   if (warp == 0) {
     int base = 0;
     Cursor c = {-1, 0, 0, 0};
-    int nv_at = 0;
     for (int b0 = 0; b0 < p.B && u0 < total; b0 += 32) {
       const int b = b0 + lane;
       const int nv = b < p.B ? seq_pages(p, seq_len(p, b)).nv : 0;
@@ -143,18 +191,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       if (hit) {
         const int l = __ffs(hit) - 1;
         const int off = u0 - __shfl_sync(0xffffffffu, lo, l);
-        nv_at = __shfl_sync(0xffffffffu, nv, l);
+        const int nv_at = __shfl_sync(0xffffffffu, nv, l);
         const int t = off / nv_at;
         c = Cursor{b0 + l, t / p.hgs, t % p.hgs, off % nv_at};
         break;
       }
       base += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) {
-      start_s = c;
-      p.desc[blockIdx.x] = WindowDesc{c.b, c.h, c.hg, c.page, nv_at, {0, 0, 0}};
-      if (blockIdx.x == 0) p.desc[p.ctas] = WindowDesc{0, 0, 0, total, share, {0, 0, 0}};
-    }
+    if (lane == 0) start_s = c;
   }
   __syncthreads();
   Cursor cur = start_s;
@@ -378,9 +422,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             a[3] &= km8;
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            // The instruction truncates its sums: over tens of thousands of rows that adds up to a
+            // bias, so the 16 rows' product is formed from zero, the small terms first, and added
+            // to the running output with rounding (error of 64K rows 5.1e-6 -> 2.5e-7).
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int t = 0; t < 3; ++t) mma16816(acc[mt][nt], a, pt[t][nt][0], pt[t][nt][1]);
+            for (int t = 2; t >= 0; --t) mma16816(o, a, pt[t][nt][0], pt[t][nt][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[mt][nt][i] += o[i];
+          }
         }
       }
       __syncwarp();
@@ -452,6 +503,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       }
     }
     consumers_sync();
+    if (!done) {
+      // The last CTA of the task to get here joins its partials, in CTA order: the sum does not
+      // depend on which one that is.
+      const int t0 = u - pb;                               // the task's first page
+      const int c0 = t0 / share, np = (t0 + vis.nv - 1) / share - c0 + 1;
+      if (tid == 0) {
+        __threadfence();
+        const uint32_t k = atomicAdd(p.arrived + c0, 1u);
+        if (k == (uint32_t)np - 1) p.arrived[c0] = 0u;
+        __threadfence();
+        last_s = k == (uint32_t)np - 1;
+      }
+      consumers_sync();
+      if (last_s) join_partials<D>(p, reinterpret_cast<float(*)[16]>(merge), inv_s, np, c0, t0 != c0 * share, heads, (size_t)b * p.Hq + hq0);
+    }
     u += pe - pb;
     cur.page = 0;
     if (pe == vis.nv && ++cur.hg == p.hgs) {
@@ -464,71 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   }
 }
 
-// Joins the partials of a task that several CTAs share, in CTA order.  CTA c of this grid looks
-// at the boundary between shares c and c + 1 and acts if it is the first boundary inside a task.
-constexpr int kMergeThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ WindowParams p) {
-  __shared__ float wts[kChunkMaxCtas][16];
-  __shared__ float inv_s[16], lse_s[16];
-  pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x + 1;
-  const WindowDesc d = p.desc[c];
-  const int share = p.desc[p.ctas].nv;
-  if (d.b < 0 || d.page == 0) return;
-  const int t0 = c * share - d.page;           // first page of the task
-  const int c0 = t0 / share, c1 = (t0 + d.nv - 1) / share;
-  if (c0 != c - 1) return;
-  const int hgw = p.hgs == 1 ? p.G : ((p.G + p.hgs - 1) / p.hgs + 1) & ~1;
-  const int heads = min(hgw, p.G - d.hg * hgw);
-  const size_t o0 = (size_t)d.b * p.Hq + d.h * p.G + d.hg * hgw;
-  const int np = c1 - c0 + 1;
-  auto slot = [&](int i) { return i == 0 ? 2 * (size_t)c0 + (t0 == c0 * share ? 0 : 1) : 2 * (size_t)(c0 + i); };
-  // 16 lanes of a half warp share a head
-  const int hd = threadIdx.x / 16, sub = threadIdx.x % 16;
-  float M = -INFINITY, L = 0.f;
-  if (hd < heads)
-    for (int i = sub; i < np; i += 16) M = fmaxf(M, p.ml[slot(i) * 16 + hd].x);
-#pragma unroll
-  for (int o = 8; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (hd < heads)
-    for (int i = sub; i < np; i += 16) {
-      const float2 x = p.ml[slot(i) * 16 + hd];
-      const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);
-      wts[i][hd] = f;
-      L += f * x.y;
-    }
-#pragma unroll
-  for (int o = 8; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (sub == 0) {
-    inv_s[hd] = L > 0.f ? 1.f / L : 0.f;
-    lse_s[hd] = L > 0.f ? M + log2f(L) : -INFINITY;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < heads * (D / 4); e += kMergeThreads) {
-    const int g = e / (D / 4), c4 = (e % (D / 4)) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < np; ++i) {
-      const float f = wts[i][g];
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + (slot(i) * 16 + g) * D + c4));
-      x.x += f * y.x;
-      x.y += f * y.y;
-      x.z += f * y.z;
-      x.w += f * y.w;
-    }
-    const float r = inv_s[g];
-    *reinterpret_cast<float4*>(p.out + (o0 + g) * D + c4) = make_float4(x.x * r, x.y * r, x.z * r, x.w * r);
-    if (c4 == 0) {
-      if (p.lse != nullptr) p.lse[o0 + g] = lse_s[g] * 0.69314718055994531f;
-      if (p.lse2 != nullptr) p.lse2[o0 + g] = lse_s[g];
-    }
-  }
-}
-
-// weights[b,h,j] += sum_g 2^(z - lse2), one thread per visible row.
-constexpr int kWeightThreads = 256;
+// weights[b,h,j] += sum_g 2^(z - lse2).  A thread takes kWeightRows visible rows, all of whose loads
+// are in flight at once (one row a thread: 17 us for 4 x 64K rows of 8 heads, four: 15.7 us).
+constexpr int kWeightThreads = 256, kWeightRows = 4;
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_constant__ WindowParams p) {
   pdl_wait();
   pdl_trigger();
@@ -537,19 +541,45 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_co
   const int n = seq_len(p, b);
   if (n == 0) return;
   const VisiblePages vis = seq_pages(p, n);
-  const int vr = blockIdx.x * kWeightThreads + threadIdx.x;
-  if (vr >= vis.nv * kPage) return;
-  const int j = vis.page(vr / kPage) * kPage + vr % kPage;
-  if (j >= n || !(p.window <= 0 || j >= vis.first || j < p.sinks)) return;
-  const float* z = p.z + ((size_t)bh * p.zcap + vr) * p.gpad;
+  const int vr0 = blockIdx.x * kWeightThreads * kWeightRows + threadIdx.x;
   const float* ls = p.lse2 + (size_t)b * p.Hq + h * p.G;
-  float s = 0.f;
-  for (int g = 0; g < p.G; g += 2) {
-    const float2 v = *reinterpret_cast<const float2*>(z + g);
-    s += ex2(v.x - ls[g]);
-    if (g + 1 < p.G) s += ex2(v.y - ls[g + 1]);
+  const float* z = p.z + (size_t)bh * p.zcap * p.gpad;
+  float* w = p.weights + (size_t)bh * p.cap;
+  int j[kWeightRows];
+  float s[kWeightRows];
+#pragma unroll
+  for (int i = 0; i < kWeightRows; ++i) {
+    const int vr = vr0 + i * kWeightThreads;
+    j[i] = -1;
+    s[i] = 0.f;
+    if (vr >= vis.nv * kPage) continue;
+    const int at = vis.page(vr / kPage) * kPage + vr % kPage;
+    if (at < n && (p.window <= 0 || at >= vis.first || at < p.sinks)) j[i] = at;
   }
-  p.weights[(size_t)bh * p.cap + j] += s;
+  if (p.G % 4 == 0) {
+    for (int g = 0; g < p.G; g += 4) {
+      const float l0 = ls[g], l1 = ls[g + 1], l2 = ls[g + 2], l3 = ls[g + 3];
+#pragma unroll
+      for (int i = 0; i < kWeightRows; ++i) {
+        if (j[i] < 0) continue;
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(z + (size_t)(vr0 + i * kWeightThreads) * p.gpad + g));
+        s[i] += ex2(v.x - l0);
+        s[i] += ex2(v.y - l1);
+        s[i] += ex2(v.z - l2);
+        s[i] += ex2(v.w - l3);
+      }
+    }
+  } else {
+    for (int g = 0; g < p.G; ++g) {
+      const float l0 = ls[g];
+#pragma unroll
+      for (int i = 0; i < kWeightRows; ++i)
+        if (j[i] >= 0) s[i] += ex2(__ldcg(z + (size_t)(vr0 + i * kWeightThreads) * p.gpad + g) - l0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kWeightRows; ++i)
+    if (j[i] >= 0) w[j[i]] += s[i];
 }
 
 template <int D, int NT>
@@ -560,12 +590,8 @@ cudaError_t launch_t(const WindowParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((unsigned)p.ctas), dim3(kThreads), (size_t)Gm::SMEM, stream, p);
   if (e != cudaSuccess) return e;
-  if (p.ctas > 1) {
-    e = launch_pdl(merge_kernel<D>, dim3((unsigned)(p.ctas - 1)), dim3(kMergeThreads), 0, stream, p);
-    if (e != cudaSuccess) return e;
-  }
   if (p.weights != nullptr)
-    return launch_pdl(weights_kernel, dim3((unsigned)((p.zcap + kWeightThreads - 1) / kWeightThreads), (unsigned)(p.B * p.Hkv)),
+    return launch_pdl(weights_kernel, dim3((unsigned)((p.zcap + kWeightThreads * kWeightRows - 1) / (kWeightThreads * kWeightRows)), (unsigned)(p.B * p.Hkv)),
                       dim3(kWeightThreads), 0, stream, p);
   return cudaSuccess;
 }
@@ -584,8 +610,7 @@ void plan_window(WindowParams& p) {
 }
 
 size_t window_workspace_bytes(const WindowParams& p, bool weights) {
-  size_t o = (size_t)(kChunkMaxCtas + 1) * sizeof(WindowDesc);
-  o += (size_t)2 * kChunkMaxCtas * 16 * (sizeof(float2) + (size_t)p.d * 4);
+  size_t o = (size_t)2 * kChunkMaxCtas * 16 * (sizeof(float2) + (size_t)p.d * 4);
   if (weights) {
     o += ((size_t)p.B * p.Hq * 4 + 255) & ~(size_t)255;
     // for any window: the capacity bounds the visible rows
@@ -596,8 +621,6 @@ size_t window_workspace_bytes(const WindowParams& p, bool weights) {
 
 void bind_window(WindowParams& p, void* scratch, bool weights) {
   unsigned char* w = static_cast<unsigned char*>(scratch);
-  p.desc = reinterpret_cast<WindowDesc*>(w);
-  w += (size_t)(kChunkMaxCtas + 1) * sizeof(WindowDesc);
   p.ml = reinterpret_cast<float2*>(w);
   w += (size_t)2 * kChunkMaxCtas * 16 * sizeof(float2);
   p.part = reinterpret_cast<float*>(w);

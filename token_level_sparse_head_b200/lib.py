@@ -117,12 +117,23 @@ def _p(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _device() -> int:
+    import torch
+
+    return torch.cuda.current_device()
+
+
+def _raw_stream(device: int) -> int:
+    """The device's current stream as a pointer (0.2 us; building a Stream object takes 3 us)."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _stream(stream=None) -> Optional[int]:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_device())
 
 
 @dataclass
