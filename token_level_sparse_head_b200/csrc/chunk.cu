@@ -40,7 +40,11 @@ struct Geo {
   static constexpr int TILE_BYTES = HALVES * HALF_BYTES;   // Q tile, K block or V block
   static constexpr int STAGES = D == 128 ? 5 : 8;
   static constexpr int SMEM = 1024 + (2 + STAGES) * TILE_BYTES;
-  static constexpr int COL_O = 256;                        // S0, S1 at columns 0 and 128
+  // Tensor memory, 512 columns: P of the tiles (64 each), S, O of the tiles.  At d = 128 the tiles
+  // share one S; at d = 64 there is room for two.
+  static constexpr int S_BUFS = D == 128 ? 1 : 2;
+  static constexpr int COL_P = 0, COL_S = 128, COL_O = 512 - 2 * D;
+  static_assert(COL_S + S_BUFS * kTile <= COL_O, "tensor memory");
 };
 
 // ----------------------------------------------------------------------------- tensor memory
@@ -55,24 +59,39 @@ __device__ __forceinline__ void tmem_ld32(float* r, uint32_t addr) {
         "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* u) {
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* u) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(u[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(u[0]),
       "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
-      "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
-      "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
-      "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
+      "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(float* r, uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const float* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(r[0]), "f"(r[1]), "f"(r[2]),
+               "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "r"(addr) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// All matrix instructions this thread has issued so far arrive on `bar` when they are done.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+// The matrix warp runs as a whole, so that descriptors are computed once per warp, and its `lead`
+// lane issues: a branch around the instructions would move each operand over by itself.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// All matrix instructions the lead lane has issued so far arrive on `bar` when they are done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
+      : "memory");
 }
 
 // Shared-memory operand of 128-byte swizzled rows.  `lead` is the distance between 64-column
@@ -85,18 +104,18 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
 constexpr uint32_t mma_form(int n, bool b_rows) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_rows ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t form, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t form, bool add, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(form), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(form), "r"((uint32_t)add), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t form, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t form, bool add, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(form), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(form), "r"((uint32_t)add), "r"(lead)
       : "memory");
 }
 
@@ -115,6 +134,9 @@ __device__ __forceinline__ bool wait_live(uint64_t* bar, uint32_t parity, volati
     }
   }
 }
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* stop) {
+  return __all_sync(0xffffffffu, wait_live(bar, parity, stop));
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -132,6 +154,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // again as 2 x 128 x 208 + 128 x 88.
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+// Not to be moved out of the branch that needs it: most blocks are visible whole.
+__device__ __forceinline__ void hide_unless(float& x, uint32_t bit) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tselp.f32 %0, %0, 0fFF800000, p;\n\t}" : "+f"(x) : "r"(bit));
+}
 // Bits 0 .. x-1 of a 64-row page.
 __device__ __forceinline__ uint64_t low_bits(int x) { return x <= 0 ? 0ull : (x >= 64 ? ~0ull : (1ull << x) - 1); }
 
@@ -252,11 +278,14 @@ __device__ __forceinline__ void next_task(Place& c, int tasks) {
   }
 }
 
-// Ring positions of the blocks of a segment of n units, counted from its first.  Two tiles: K0 V0
-// K1 V1 ...; one tile: K0 K1, then V(2j) K(2j+2) V(2j+1) K(2j+3) for unit j: the order of use.
-__device__ __forceinline__ int ring_k(bool one, int j, int t) { return !one ? 2 * j : (j == 0 ? t : 4 * j - 1 + 2 * t); }
-__device__ __forceinline__ int ring_v(bool one, int j, int t, int n) {
-  return !one ? 2 * j + 1 : 4 * j + 2 + (j + 1 < n ? 2 * t : t);
+// Ring positions of the blocks of a segment of n units, counted from its first, in the order of
+// use.  Two tiles: K0, then K(j+1) V(j) for unit j; one tile: both warpgroups' K0, then for unit
+// j and each warpgroup K(j+1) V(j).
+__device__ __forceinline__ int ring_k(bool one, int j, int x) {
+  return one ? (j == 0 ? x : 4 * j - 2 + 2 * x) : (j == 0 ? 0 : 2 * j - 1);
+}
+__device__ __forceinline__ int ring_v(bool one, int j, int x, int n) {
+  return one ? (j + 1 < n ? 4 * j + 3 + 2 * x : 4 * j + 2 + x) : (j + 1 < n ? 2 * j + 2 : 2 * j + 1);
 }
 
 template <int D>
@@ -266,11 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   extern __shared__ unsigned char smem_raw[];
   unsigned char* qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* ring = qs + 2 * Gm::TILE_BYTES;
-  __shared__ uint64_t full[ST], empty[ST], q_full, q_empty, s_full[2], p_ready[2], o_full[2], half_full, half_free, drain;
+  __shared__ uint64_t full[ST], empty[ST], q_full, q_empty, s_full[2], s_read[2], p_ready[2], pv_done[2], half_full, half_free, drain;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int stop_s;
   __shared__ Place start_s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
@@ -282,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_ready[t], 4);
-      mbar_init(&o_full[t], 1);
+      mbar_init(&s_read[t], 4);
+      mbar_init(&pv_done[t], 1);
     }
     mbar_init(&half_full, 4);
     mbar_init(&half_free, 4);
@@ -375,12 +405,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         push(&p.kmap, 4 * c.block + 2);
         for (int j = c.block; j < be; ++j)
           for (int x = 0; x < 2; ++x) {
-            push(&p.vmap, 4 * j + 2 * x);
             if (j + 1 < be) push(&p.kmap, 4 * j + 4 + 2 * x);
+            push(&p.vmap, 4 * j + 2 * x);
           }
       } else {
+        push(&p.kmap, 2 * c.block);
         for (int j = c.block; j < be; ++j) {
-          push(&p.kmap, 2 * j);
+          if (j + 1 < be) push(&p.kmap, 2 * j + 2);
           push(&p.vmap, 2 * j);
         }
       }
@@ -394,62 +425,66 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- matrix instructions
-    if (lane == 0) {
+    {
+      const uint32_t lead = elect_lane();
       constexpr uint32_t kFormS = mma_form(kTile, false), kFormO = mma_form(D, true);
       const uint32_t qb = smem_u32(qs), rb = smem_u32(ring);
-      int base = 0, seg = 0;
+      int base = 0, seg = 0, s_uses = 0;
       uint32_t ph_p[2] = {0, 0};
       bool live = true;
-      auto stage = [&](int idx) { return idx % ST; };
-      auto scores = [&](int x, bool one, int idx) {  // S_x = Q K^T
-        const int st = stage(idx);
-        live = live && wait_live(&full[st], (idx / ST) & 1, &stop_s);
+      auto scores = [&](int x, bool one, int idx) {  // S = Q K^T for warpgroup x
+        const int st = idx % ST, buf = Gm::S_BUFS == 1 ? 0 : x;
+        // the scores that were there before have been read
+        if (s_uses >= Gm::S_BUFS) live = live && wait_warp(&s_read[buf], ((s_uses / Gm::S_BUFS) & 1) ^ 1, &stop_s);
+        ++s_uses;
+        live = live && wait_warp(&full[st], (idx / ST) & 1, &stop_s);
         if (!live) return;
         tc_fence_after();
         const uint32_t a = qb + (one ? 0 : x) * Gm::TILE_BYTES, b = rb + st * Gm::TILE_BYTES;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t o = (k >> 2) * Gm::HALF_BYTES + (k & 3) * 32;
-          mma_ss(tmem + x * kTile, operand(a + o, 16), operand(b + o, 16), kFormS, k > 0);
+          mma_ss(tmem + Gm::COL_S + buf * kTile, operand(a + o, 16), operand(b + o, 16), kFormS, k > 0, lead);
         }
-        tc_commit(&s_full[x]);
-        if (one || x == 1) tc_commit(&empty[st]);
+        tc_commit(&s_full[x], lead);
+        if (one || x == 1) tc_commit(&empty[st], lead);
       };
       for (long long u = u0; u < u1 && live; ++seg) {
         const ChunkTask t = p.tasks[c.task];
         const int n = (int)min((long long)t.blocks - c.block, u1 - u);
         const bool one = t.ntok <= p.tok_tile;
-        live = wait_live(&q_full, seg & 1, &stop_s);
+        live = wait_warp(&q_full, seg & 1, &stop_s);
         scores(0, one, base + ring_k(one, 0, 0));
         scores(1, one, base + ring_k(one, 0, 1));
-        if (n == 1 && live) tc_commit(&q_empty);
+        if (n == 1 && live) tc_commit(&q_empty, lead);
         for (int j = 0; j < n && live; ++j)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            live = live && wait_live(&p_ready[x], ph_p[x], &stop_s);
+            // the next block's scores go before this block's output: the softmax need not wait for either
+            if (j + 1 < n) {
+              scores(x, one, base + ring_k(one, j + 1, x));
+              if (j + 2 == n && x == 1 && live) tc_commit(&q_empty, lead);
+            }
+            const int idx = base + ring_v(one, j, x, n), st = idx % ST;
+            live = live && wait_warp(&p_ready[x], ph_p[x], &stop_s);
             ph_p[x] ^= 1;
-            const int idx = base + ring_v(one, j, x, n), st = stage(idx);
-            live = live && wait_live(&full[st], (idx / ST) & 1, &stop_s);
+            live = live && wait_warp(&full[st], (idx / ST) & 1, &stop_s);
             if (!live) break;
             tc_fence_after();
             const uint32_t b = rb + st * Gm::TILE_BYTES;
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(tmem + Gm::COL_O + x * D, tmem + x * kTile + k * 8, operand(b + k * 2048, Gm::HALF_BYTES), kFormO, j > 0 || k > 0);
-            if (one || x == 1) tc_commit(&empty[st]);
-            if (j + 1 < n) {
-              scores(x, one, base + ring_k(one, j + 1, x));
-              if (j + 2 == n && x == 1 && live) tc_commit(&q_empty);
-            } else {
-              tc_commit(&o_full[x]);
-            }
+              mma_ts(tmem + Gm::COL_O + x * D, tmem + Gm::COL_P + x * (kTile / 2) + k * 8, operand(b + k * 2048, Gm::HALF_BYTES),
+                     kFormO, j > 0 || k > 0, lead);
+            tc_commit(&pv_done[x], lead);
+            if (one || x == 1) tc_commit(&empty[st], lead);
           }
         base += (one ? 4 : 2) * n;
         u += n;
         next_task(c, tasks);
       }
       // every product has left shared and tensor memory before they are given back
-      tc_commit(&drain);
+      tc_commit(&drain, lead);
       mbar_wait_bounded(&drain, 0);
     }
     __syncwarp();
@@ -458,7 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     regs_up();
     const int x = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + x * kTile + lanes, tO = tmem + Gm::COL_O + x * D + lanes;
+    const int s_buf = Gm::S_BUFS == 1 ? 0 : x;
+    const uint32_t tS = tmem + Gm::COL_S + s_buf * kTile + lanes, tP = tmem + Gm::COL_P + x * (kTile / 2) + lanes,
+                   tO = tmem + Gm::COL_O + x * D + lanes;
     const float scale = p.scale_log2, grow_by = 8.f / scale;
     int base = 0;
     uint32_t ph_s = 0, ph_o = 0, ph_half = 0;
@@ -479,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
       for (int j = 0; j < n; ++j) {
         const int v0 = one ? (c.block + j) * 4 + 2 * x : (c.block + j) * 2;
-        live = __all_sync(0xffffffffu, wait_live(&s_full[x], ph_s, &stop_s));
+        live = wait_warp(&s_full[x], ph_s, &stop_s);
         ph_s ^= 1;
         if (!live) break;
         tc_fence_after();
@@ -498,9 +535,75 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             dirty = dirty || j0 + kPage > n_seq || (j0 < vis.first && j0 + kPage > p.sinks);
           }
         }
+        float s[kTile];
+        if (busy) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s + 32 * i, tS + 32 * i);
+          tmem_wait_ld();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_read[s_buf]);
+        bool grow = false;
+        float f = 1.f;
+        if (busy) {
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint64_t see = 0;
+              if (mine && at[i] >= 0)
+                see = low_bits(pos + 1 - at[i]) & (~low_bits(wlo - at[i]) | low_bits(p.sinks - at[i]));
+              const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                hide_unless(s[64 * i + e], lo & (1u << e));
+                hide_unless(s[64 * i + 32 + e], hi & (1u << e));
+              }
+            }
+          }
+          float mx[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = max3(s[e], s[8 + e], s[16 + e]);
+#pragma unroll
+          for (int i = 24; i < kTile - 8; i += 16)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 8 + e]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = fmaxf(mx[e], s[kTile - 8 + e]);
+          const float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[4]), max3(mx[5], mx[6], mx[7]));
+          grow = __any_sync(0xffffffffu, mine && top > m + grow_by);
+          if (grow) {
+            const float mn = fmaxf(m, top);
+            f = m == -INFINITY ? 0.f : ex2((m - mn) * scale);
+            l *= f;
+            m = mn;
+          }
+          const float off = m == -INFINITY ? 0.f : -m * scale;
+          const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
+          float2 sum[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < kTile / 2; ++e) {
+            float2 z = ffma2(make_float2(s[2 * e], s[2 * e + 1]), sc2, off2);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            sum[e & 3] = __fadd2_rn(sum[e & 3], z);
+            s[e] = __uint_as_float(pack_bf16(z.x, z.y));
+          }
+          sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+          l += sum[0].x + sum[0].y;
+        }
+        // the product of the block before has read P, and O may be scaled
+        if (j > 0) {
+          live = wait_warp(&pv_done[x], ph_o, &stop_s);
+          ph_o ^= 1;
+          if (!live) break;
+          tc_fence_after();
+        }
         if (dirty) {
           const int idx = base + ring_v(one, j, x, n), st = idx % ST;
-          live = __all_sync(0xffffffffu, wait_live(&full[st], (idx / ST) & 1, &stop_s));
+          live = wait_warp(&full[st], (idx / ST) & 1, &stop_s);
           if (!live) break;
           const int a = r < 64 ? at[0] : at[1], pj = a + (r & 63);
           if (a >= 0 && (pj >= n_seq || (pj < vis.first && pj >= p.sinks))) {
@@ -513,67 +616,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         if (busy) {
-          float s[kTile];
+          if (grow && j > 0) {
+#pragma unroll 1
+            for (int i = 0; i < D / 8; ++i) {
+              float o[8];
+              tmem_ld8(o, tO + 8 * i);
+              tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s + 32 * i, tS + 32 * i);
-          tmem_wait_ld();
-          if (!whole) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint64_t see = 0;
-              if (mine && at[i] >= 0)
-                see = low_bits(pos + 1 - at[i]) & (~low_bits(wlo - at[i]) | low_bits(p.sinks - at[i]));
-              const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                if (!((lo >> e) & 1)) s[64 * i + e] = -INFINITY;
-                if (!((hi >> e) & 1)) s[64 * i + 32 + e] = -INFINITY;
-              }
+              for (int e = 0; e < 8; ++e) o[e] *= f;
+              tmem_st8(tO + 8 * i, o);
             }
           }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 4; i < kTile - 4; i += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kTile - 4 + e]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (__any_sync(0xffffffffu, mine && top > m + grow_by)) {
-            const float mn = fmaxf(m, top);
-            if (j > 0) {
-              // S(j) is complete, so P V of block j - 1, issued before it, is too
-              const float f = m == -INFINITY ? 0.f : ex2((m - mn) * scale);
-              l *= f;
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i) {
-                float o[32];
-                tmem_ld32(o, tO + 32 * i);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tmem_st32(tO + 32 * i, reinterpret_cast<const uint32_t*>(o));
-              }
-            }
-            m = mn;
-          }
-          const float off = m == -INFINITY ? 0.f : -m * scale;
-          const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t w[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float2 z = ffma2(make_float2(s[64 * i + 2 * e], s[64 * i + 2 * e + 1]), sc2, off2);
-              z.x = ex2(z.x);
-              z.y = ex2(z.y);
-              sum[e & 1] = __fadd2_rn(sum[e & 1], z);
-              w[e] = pack_bf16(z.x, z.y);
-            }
-            tmem_st32(tS + 32 * i, w);
-          }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          for (int i = 0; i < 4; ++i) tmem_st16(tP + 16 * i, reinterpret_cast<const uint32_t*>(s) + 16 * i);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -583,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       if (!live) break;
 
       // ---- this segment's rows ----
-      live = __all_sync(0xffffffffu, wait_live(&o_full[x], ph_o, &stop_s));
+      live = wait_warp(&pv_done[x], ph_o, &stop_s);
       ph_o ^= 1;
       if (!live) break;
       tc_fence_after();
@@ -594,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const float mz = m == -INFINITY ? m : m * scale;
       if (!done || (one && x == 1)) {
         if (done && half_used) {  // the other warpgroup has read the half it got before
-          live = __all_sync(0xffffffffu, wait_live(&half_free, ph_half ^ 1, &stop_s));
+          live = wait_warp(&half_free, ph_half ^ 1, &stop_s);
           if (!live) break;
         }
         if (busy) {
@@ -620,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       } else {
         float f0 = 1.f, f1 = 0.f, M = mz, L = l;
         if (one) {
-          live = __all_sync(0xffffffffu, wait_live(&half_full, ph_half, &stop_s));
+          live = wait_warp(&half_full, ph_half, &stop_s);
           ph_half ^= 1;
           if (!live) break;
           if (mine) {
