@@ -120,20 +120,23 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 
 // ----------------------------------------------------------------------------- waits
-// Waits for a phase; gives up when another warp has or after a few seconds' worth of cycles.
-constexpr long long kWaitCycles = 4000000000LL;
+// Waits for a phase; gives up when another warp has or after the library's limit.  Each lane waits
+// for itself: a vote after every wait costs as much as the wait.
 __device__ __forceinline__ bool wait_live(uint64_t* bar, uint32_t parity, volatile int* stop) {
   if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (;;) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*stop) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *stop = 1;
-      return false;
-    }
+    if ((i & 15u) == 15u && *stop) return false;
   }
+  *stop = 1;
+  return false;
 }
+__device__ __forceinline__ void wait_row(uint64_t* bar, uint32_t parity, volatile int* stop) {
+  wait_live(bar, parity, stop);
+  __syncwarp();
+}
+// The matrix warp's: the same answer for all lanes.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* stop) {
   return __all_sync(0xffffffffu, wait_live(bar, parity, stop));
 }
@@ -278,12 +281,23 @@ __device__ __forceinline__ void next_task(Place& c, int tasks) {
   }
 }
 
-// Ring positions of the blocks of a segment of n units, counted from its first, in the order of
-// use.  Two tiles: K0, then K(j+1) V(j) for unit j; one tile: both warpgroups' K0, then for unit
-// j and each warpgroup K(j+1) V(j).
-__device__ __forceinline__ int ring_k(bool one, int j, int x) {
-  return one ? (j == 0 ? x : 4 * j - 2 + 2 * x) : (j == 0 ? 0 : 2 * j - 1);
-}
+// A place in the ring and the parity of its turn; blocks lie in it in the order of use.  Two tiles:
+// K0, then K(j+1) V(j) for unit j; one tile: both warpgroups' K0, then for unit j and each
+// warpgroup K(j+1) V(j).
+struct Ring {
+  int st;
+  uint32_t ph;
+  template <int ST>
+  __device__ __forceinline__ Ring take() {
+    const Ring x = *this;
+    if (++st == ST) {
+      st = 0;
+      ph ^= 1;
+    }
+    return x;
+  }
+};
+// Position of V of unit j among the blocks of a segment of n units.
 __device__ __forceinline__ int ring_v(bool one, int j, int x, int n) {
   return one ? (j + 1 < n ? 4 * j + 3 + 2 * x : 4 * j + 2 + x) : (j + 1 < n ? 2 * j + 2 : 2 * j + 1);
 }
@@ -426,60 +440,68 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   } else if (warp == 8) {
     // ---------------------------------------------------------------- matrix instructions
     {
+      // The scores' buffer goes back and forth between this warp and the softmax: what does not
+      // depend on a wait is done before it.
       const uint32_t lead = elect_lane();
       constexpr uint32_t kFormS = mma_form(kTile, false), kFormO = mma_form(D, true);
-      const uint32_t qb = smem_u32(qs), rb = smem_u32(ring);
-      int base = 0, seg = 0, s_uses = 0;
-      uint32_t ph_p[2] = {0, 0};
+      const uint64_t qd = operand(smem_u32(qs), 16), kd = operand(smem_u32(ring), 16), vd = operand(smem_u32(ring), Gm::HALF_BYTES);
+      constexpr uint32_t kStep = Gm::TILE_BYTES >> 4;
+      int seg = 0;
+      Ring r = {0, 0}, k, v;
+      uint32_t ph_p = 0, ph_read = 1;  // parity of the scores' reads: the first use of a buffer waits for none
       bool live = true;
-      auto scores = [&](int x, bool one, int idx) {  // S = Q K^T for warpgroup x
-        const int st = idx % ST, buf = Gm::S_BUFS == 1 ? 0 : x;
-        // the scores that were there before have been read
-        if (s_uses >= Gm::S_BUFS) live = live && wait_warp(&s_read[buf], ((s_uses / Gm::S_BUFS) & 1) ^ 1, &stop_s);
-        ++s_uses;
-        live = live && wait_warp(&full[st], (idx / ST) & 1, &stop_s);
+      auto scores = [&](int x, bool one) {  // S = Q K^T for warpgroup x, K in ring place k
+        const int buf = Gm::S_BUFS == 1 ? 0 : x;
+        const uint64_t a = qd + (one ? 0 : x) * kStep, b = kd + k.st * kStep;
+        live = live && wait_warp(&full[k.st], k.ph, &stop_s);
+        live = live && wait_warp(&s_read[buf], ph_read, &stop_s);  // the scores that were there have been read
+        if (Gm::S_BUFS == 1 || x == 1) ph_read ^= 1;
         if (!live) return;
         tc_fence_after();
-        const uint32_t a = qb + (one ? 0 : x) * Gm::TILE_BYTES, b = rb + st * Gm::TILE_BYTES;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = (k >> 2) * Gm::HALF_BYTES + (k & 3) * 32;
-          mma_ss(tmem + Gm::COL_S + buf * kTile, operand(a + o, 16), operand(b + o, 16), kFormS, k > 0, lead);
+        for (int i = 0; i < D / 16; ++i) {
+          constexpr int kHalf = Gm::HALF_BYTES >> 4;
+          const uint32_t o = (i >> 2) * kHalf + (i & 3) * 2;
+          mma_ss(tmem + Gm::COL_S + buf * kTile, a + o, b + o, kFormS, i > 0, lead);
         }
         tc_commit(&s_full[x], lead);
-        if (one || x == 1) tc_commit(&empty[st], lead);
+        if (one || x == 1) tc_commit(&empty[k.st], lead);
       };
       for (long long u = u0; u < u1 && live; ++seg) {
         const ChunkTask t = p.tasks[c.task];
         const int n = (int)min((long long)t.blocks - c.block, u1 - u);
         const bool one = t.ntok <= p.tok_tile;
         live = wait_warp(&q_full, seg & 1, &stop_s);
-        scores(0, one, base + ring_k(one, 0, 0));
-        scores(1, one, base + ring_k(one, 0, 1));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x == 0 || one) k = r.take<ST>();
+          scores(x, one);
+        }
         if (n == 1 && live) tc_commit(&q_empty, lead);
-        for (int j = 0; j < n && live; ++j)
+        for (int j = 0; j < n && live; ++j) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             // the next block's scores go before this block's output: the softmax need not wait for either
             if (j + 1 < n) {
-              scores(x, one, base + ring_k(one, j + 1, x));
+              if (x == 0 || one) k = r.take<ST>();
+              scores(x, one);
               if (j + 2 == n && x == 1 && live) tc_commit(&q_empty, lead);
             }
-            const int idx = base + ring_v(one, j, x, n), st = idx % ST;
-            live = live && wait_warp(&p_ready[x], ph_p[x], &stop_s);
-            ph_p[x] ^= 1;
-            live = live && wait_warp(&full[st], (idx / ST) & 1, &stop_s);
+            if (x == 0 || one) v = r.take<ST>();
+            const uint64_t b = vd + v.st * kStep;
+            live = live && wait_warp(&full[v.st], v.ph, &stop_s);
+            live = live && wait_warp(&p_ready[x], ph_p, &stop_s);
             if (!live) break;
             tc_fence_after();
-            const uint32_t b = rb + st * Gm::TILE_BYTES;
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(tmem + Gm::COL_O + x * D, tmem + Gm::COL_P + x * (kTile / 2) + k * 8, operand(b + k * 2048, Gm::HALF_BYTES),
-                     kFormO, j > 0 || k > 0, lead);
+            for (int i = 0; i < kTile / 16; ++i)
+              mma_ts(tmem + Gm::COL_O + x * D, tmem + Gm::COL_P + x * (kTile / 2) + i * 8, b + i * (2048 >> 4), kFormO,
+                     j > 0 || i > 0, lead);
             tc_commit(&pv_done[x], lead);
-            if (one || x == 1) tc_commit(&empty[st], lead);
+            if (one || x == 1) tc_commit(&empty[v.st], lead);
           }
-        base += (one ? 4 : 2) * n;
+          ph_p ^= 1;
+        }
         u += n;
         next_task(c, tasks);
       }
@@ -499,8 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const float scale = p.scale_log2, grow_by = 8.f / scale;
     int base = 0;
     uint32_t ph_s = 0, ph_o = 0, ph_half = 0;
-    bool live = true, half_used = false;
-    for (long long u = u0; u < u1 && live;) {
+    bool half_used = false;
+    // After a wait that ran out the waits below return at once and what is computed does not count.
+    for (long long u = u0; u < u1;) {
       const ChunkTask t = p.tasks[c.task];
       const int n_seq = t.seqlen;
       const int n = (int)min((long long)t.blocks - c.block, u1 - u);
@@ -513,28 +536,43 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int tok = r / p.G, pos = plo + tok;
       const int wlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;  // first of the row's window
       float m = -INFINITY, l = 0.f;
+      // Blocks plain0 .. plain1 - 1 of the segment lie inside the window of every row, whole: pages
+      // from pg0 to pg1 - 1 of the sequence, behind the sinks' pages of the list.
+      int plain0, plain1;
+      {
+        const int pg0 = max(vis.w0, p.window > 0 ? (max(0, phi - p.window + 1) + kPage - 1) / kPage : 0);
+        const int pg1 = (plo + 1) / kPage;
+        const int a0 = pg0 - vis.w0 + vis.ns, a1 = pg1 - vis.w0 + vis.ns;  // in the list
+        if (one) {
+          plain0 = ((a0 - 2 * x + 3) >> 2) - c.block;
+          plain1 = ((a1 - 2 * x + 2) >> 2) - c.block;
+        } else {
+          plain0 = ((a0 + 1) >> 1) - c.block;
+          plain1 = (a1 >> 1) - c.block;
+        }
+      }
 
       for (int j = 0; j < n; ++j) {
         const int v0 = one ? (c.block + j) * 4 + 2 * x : (c.block + j) * 2;
-        live = wait_warp(&s_full[x], ph_s, &stop_s);
-        ph_s ^= 1;
-        if (!live) break;
-        tc_fence_after();
         bool whole = true, dirty = false;
-        int at[2];
+        int at[2] = {0, 0};
+        if (j < plain0 || j >= plain1) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int j0 = vis.page(v0 + i) * kPage;
-          at[i] = v0 + i < vis.nv ? j0 : -1;
-          if (v0 + i >= vis.nv) {
-            whole = false;
-          } else {
-            whole = whole && j0 + kPage - 1 <= plo &&
-                    (p.window <= 0 || j0 > phi - p.window || j0 + kPage <= p.sinks);
-            // rows that no token sees may hold anything, and 0 * NaN is not 0
-            dirty = dirty || j0 + kPage > n_seq || (j0 < vis.first && j0 + kPage > p.sinks);
+          for (int i = 0; i < 2; ++i) {
+            const int j0 = vis.page(v0 + i) * kPage;
+            at[i] = v0 + i < vis.nv ? j0 : -1;
+            if (v0 + i >= vis.nv) {
+              whole = false;
+            } else {
+              whole = whole && j0 + kPage - 1 <= plo && (p.window <= 0 || j0 > phi - p.window || j0 + kPage <= p.sinks);
+              // rows that no token sees may hold anything, and 0 * NaN is not 0
+              dirty = dirty || j0 + kPage > n_seq || (j0 < vis.first && j0 + kPage > p.sinks);
+            }
           }
         }
+        wait_row(&s_full[x], ph_s, &stop_s);
+        ph_s ^= 1;
+        tc_fence_after();
         float s[kTile];
         if (busy) {
 #pragma unroll
@@ -578,33 +616,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             l *= f;
             m = mn;
           }
-          const float off = m == -INFINITY ? 0.f : -m * scale;
-          const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
-          float2 sum[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int e = 0; e < kTile / 2; ++e) {
-            float2 z = ffma2(make_float2(s[2 * e], s[2 * e + 1]), sc2, off2);
-            z.x = ex2(z.x);
-            z.y = ex2(z.y);
-            sum[e & 3] = __fadd2_rn(sum[e & 3], z);
-            s[e] = __uint_as_float(pack_bf16(z.x, z.y));
-          }
-          sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-          l += sum[0].x + sum[0].y;
         }
-        // the product of the block before has read P, and O may be scaled
+        // The product of the block before has read P, and O may be scaled.
         if (j > 0) {
-          live = wait_warp(&pv_done[x], ph_o, &stop_s);
+          wait_row(&pv_done[x], ph_o, &stop_s);
           ph_o ^= 1;
-          if (!live) break;
           tc_fence_after();
         }
         if (dirty) {
           const int idx = base + ring_v(one, j, x, n), st = idx % ST;
-          live = wait_warp(&full[st], (idx / ST) & 1, &stop_s);
-          if (!live) break;
+          wait_row(&full[st], (idx / ST) & 1, &stop_s);
           const int a = r < 64 ? at[0] : at[1], pj = a + (r & 63);
           if (a >= 0 && (pj >= n_seq || (pj < vis.first && pj >= p.sinks))) {
             unsigned char* z = ring + (size_t)st * Gm::TILE_BYTES + r * 128;
@@ -618,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (busy) {
           if (grow && j > 0) {
 #pragma unroll 1
-            for (int i = 0; i < D / 8; ++i) {
+            for (int i = 0; i < D / 8; ++i) {  // 8 columns at a time: the scores stay in registers
               float o[8];
               tmem_ld8(o, tO + 8 * i);
               tmem_wait_ld();
@@ -627,20 +648,36 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               tmem_st8(tO + 8 * i, o);
             }
           }
+          const float off = m == -INFINITY ? 0.f : -m * scale;
+          const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
+          float2 sum[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_st16(tP + 16 * i, reinterpret_cast<const uint32_t*>(s) + 16 * i);
-          tmem_wait_st();
+          for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 z = ffma2(make_float2(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), sc2, off2);
+              z.x = ex2(z.x);
+              z.y = ex2(z.y);
+              sum[e & 3] = __fadd2_rn(sum[e & 3], z);
+              w[e] = pack_bf16(z.x, z.y);
+            }
+            tmem_st16(tP + 16 * i, w);
+          }
+          sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+          l += sum[0].x + sum[0].y;
         }
+        if (busy) tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_ready[x]);
       }
-      if (!live) break;
 
       // ---- this segment's rows ----
-      live = wait_warp(&pv_done[x], ph_o, &stop_s);
+      wait_row(&pv_done[x], ph_o, &stop_s);
       ph_o ^= 1;
-      if (!live) break;
       tc_fence_after();
       const bool done = n == t.blocks;
       const int slot = 2 * (int)blockIdx.x + (u == u0 ? 0 : 1);
@@ -649,8 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const float mz = m == -INFINITY ? m : m * scale;
       if (!done || (one && x == 1)) {
         if (done && half_used) {  // the other warpgroup has read the half it got before
-          live = wait_warp(&half_free, ph_half ^ 1, &stop_s);
-          if (!live) break;
+          wait_row(&half_free, ph_half ^ 1, &stop_s);
         }
         if (busy) {
           const int at = x * kTile + r;
@@ -675,9 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       } else {
         float f0 = 1.f, f1 = 0.f, M = mz, L = l;
         if (one) {
-          live = wait_warp(&half_full, ph_half, &stop_s);
+          wait_row(&half_full, ph_half, &stop_s);
           ph_half ^= 1;
-          if (!live) break;
           if (mine) {
             const float2 y = __ldcg(ml + kTile + r);
             M = fmaxf(mz, y.x);
