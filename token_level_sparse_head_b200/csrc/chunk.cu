@@ -31,6 +31,8 @@ constexpr int kPlanThreads = 1024;
 constexpr int kTile = 128;
 constexpr int kMergeRows = 32;
 constexpr int kMergeThreads = 256;
+constexpr long long kLiveBytes = 48LL << 20;
+constexpr int kWaveUnits = 24;
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D>
@@ -194,6 +196,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int span = 2 * p.tok_tile;
   int base = 0;
+  __shared__ unsigned long long keys_s;  // rows that the chunks see, one KV head
+  if (tid == 0) keys_s = 0;
+  __syncthreads();
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     int cnt = 0;
@@ -217,6 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const int k0 = off_s[i], k1 = off_s[i + 1];
       if (k0 >= k1) continue;
       const int s0 = p.q_start[b0 + i], T = p.q_start[b0 + i + 1] - s0, n = p.seqlens[b0 + i];
+      if (lane == 0) atomicAdd(&keys_s, (unsigned long long)visible_pages(n - T, n - 1, p.window, p.sinks).nv * kPage);
       for (int k = k0 + lane; k < k1; k += 32) {
         const int at = (k - k0) * span;
         ChunkTask t;
@@ -246,6 +252,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   if (tid == 0) {
     ChunkTask t = {};
     t.b = base;
+    // Waves of at most kLiveBytes of K and V, where the blocks are read more than once and a
+    // CTA's share of a wave stays long against the cost of a partial.
+    const long long once = (long long)keys_s * p.d * 4 * p.Hkv, block = (long long)kTile * p.d * 4;
+    int waves = 1;
+    if (units * p.Hkv * block > once + once / 2)
+      while (waves < p.waves_max && once > waves * kLiveBytes && units * p.Hkv > (long long)(waves + 1) * p.ctas * kWaveUnits) ++waves;
+    t.tok0 = waves;
     t.unit0 = units;
     p.tasks[p.slots] = t;
   }
@@ -255,6 +268,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 struct Place {
   int task, h, block;
 };
+// The KV heads are gone through in waves, so that the K and V that several tasks read stay in L2
+// meanwhile.  A CTA's share of a wave: units u0 .. u1 - 1 of it, the first of them at `at`.
+struct Share {
+  long long u0, u1;
+  Place at;
+};
+struct Wave {
+  long long total, share;
+  int head0;
+};
+__device__ __forceinline__ Wave wave_of(const ChunkParams& p, int w, int waves, long long units) {
+  Wave x;
+  x.head0 = w * p.Hkv / waves;
+  x.total = units * ((w + 1) * p.Hkv / waves - x.head0);
+  x.share = (x.total + p.ctas - 1) / p.ctas;
+  return x;
+}
 // Task, KV head and unit of the task at global unit u; whole warp.
 __device__ __forceinline__ Place find_unit(const ChunkParams& p, long long u, int tasks, long long units) {
   const int lane = threadIdx.x & 31;
@@ -312,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   __shared__ uint64_t full[ST], empty[ST], q_full, q_empty, s_full[2], s_read[2], p_ready[2], pv_done[2], half_full, half_free, drain;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int stop_s;
-  __shared__ Place start_s;
+  __shared__ Share share_s[kChunkMaxWaves];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   if (tid == 0) {
@@ -342,24 +372,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   pdl_trigger();
   const int tasks = p.tasks[p.slots].b;
   const long long units = p.tasks[p.slots].unit0;
-  const long long total = units * p.Hkv, share = (total + p.ctas - 1) / p.ctas;
-  const long long u0 = min(share * blockIdx.x, total), u1 = min(u0 + share, total);
-  if (warp == 0 && u0 < u1) {
-    const Place c = find_unit(p, u0, tasks, units);
-    if (lane == 0) start_s = c;
+  const int waves = p.tasks[p.slots].tok0;
+  if (warp < waves) {
+    const Wave w = wave_of(p, warp, waves, units);
+    Share x;
+    x.u0 = min(w.share * blockIdx.x, w.total);
+    x.u1 = min(x.u0 + w.share, w.total);
+    if (x.u0 < x.u1) x.at = find_unit(p, x.u0, tasks, units);
+    x.at.h += w.head0;
+    if (lane == 0) share_s[warp] = x;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
-  Place c = start_s;
 
   if (warp >= 8) regs_down();
   if (warp == 9) {
     // ---------------------------------------------------------------- loads
     int cnt = 0, seg = 0;  // blocks and Q tiles asked for
     bool live = true;
-    for (long long u = u0; u < u1 && live;) {
+    for (int w = 0; w < waves; ++w) {
+    Place c = share_s[w].at;
+    const long long u1 = share_s[w].u1;
+    for (long long u = share_s[w].u0; u < u1 && live;) {
       const ChunkTask t = p.tasks[c.task];
       const int be = (int)min((long long)t.blocks, c.block + (u1 - u)), units_here = be - c.block;
       const bool one = t.ntok <= p.tok_tile;
@@ -432,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       u += units_here;
       next_task(c, tasks);
     }
+    }
     // after a wait that ran out: the copies in flight land before the CTA ends
     if (lane == 0 && !live) {
       if (seg > 0) mbar_wait_bounded(&q_full, (seg - 1) & 1);
@@ -467,7 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         tc_commit(&s_full[x], lead);
         if (one || x == 1) tc_commit(&empty[k.st], lead);
       };
-      for (long long u = u0; u < u1 && live; ++seg) {
+      for (int w = 0; w < waves; ++w) {
+      Place c = share_s[w].at;
+      const long long u1 = share_s[w].u1;
+      for (long long u = share_s[w].u0; u < u1 && live; ++seg) {
         const ChunkTask t = p.tasks[c.task];
         const int n = (int)min((long long)t.blocks - c.block, u1 - u);
         const bool one = t.ntok <= p.tok_tile;
@@ -505,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         u += n;
         next_task(c, tasks);
       }
+      }
       // every product has left shared and tensor memory before they are given back
       tc_commit(&drain, lead);
       mbar_wait_bounded(&drain, 0);
@@ -523,6 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     uint32_t ph_s = 0, ph_o = 0, ph_half = 0;
     bool half_used = false;
     // After a wait that ran out the waits below return at once and what is computed does not count.
+    for (int w = 0; w < waves; ++w) {
+    Place c = share_s[w].at;
+    const long long u0 = share_s[w].u0, u1 = share_s[w].u1;
     for (long long u = u0; u < u1;) {
       const ChunkTask t = p.tasks[c.task];
       const int n_seq = t.seqlen;
@@ -680,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       ph_o ^= 1;
       tc_fence_after();
       const bool done = n == t.blocks;
-      const int slot = 2 * (int)blockIdx.x + (u == u0 ? 0 : 1);
+      const int slot = 2 * (w * p.ctas + (int)blockIdx.x) + (u == u0 ? 0 : 1);
       float4* part = reinterpret_cast<float4*>(p.part) + (size_t)slot * (D / 4) * p.rows_cap;
       float2* ml = p.ml + (size_t)slot * p.rows_cap;
       const float mz = m == -INFINITY ? m : m * scale;
@@ -757,6 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       u += n;
       next_task(c, tasks);
     }
+    }
     tc_fence_before();
   }
   __syncthreads();
@@ -765,8 +810,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   if (tid == 0 && stop_s) record_error(p.err, kDevWaitTimeout, blockIdx.x);
 }
 
-// Joins the partials of a task that several CTAs share, in CTA order.  blockIdx.x + 1 is the
-// share whose beginning is looked at: the first one inside a task acts for it, 32 rows a CTA.
+// Joins the partials of a task that several CTAs share, in CTA order.  blockIdx.x names
+// the wave and the share whose beginning is looked at: the first one inside a task acts for it, 32 rows a CTA.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ ChunkParams p) {
   __shared__ Place at_s;
@@ -774,20 +819,23 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   pdl_trigger();
   const int tasks = p.tasks[p.slots].b;
   const long long units = p.tasks[p.slots].unit0;
-  const long long total = units * p.Hkv, share = (total + p.ctas - 1) / p.ctas;
-  const long long u = share * (blockIdx.x + 1);
-  if (u >= total) return;
+  const int waves = p.tasks[p.slots].tok0, wi = (int)blockIdx.x / (p.ctas - 1), cta = (int)blockIdx.x % (p.ctas - 1);
+  if (wi >= waves) return;
+  const Wave wave = wave_of(p, wi, waves, units);
+  const long long share = wave.share, u = share * (cta + 1);
+  if (u >= wave.total) return;
   if (threadIdx.x < 32) {
     const Place c = find_unit(p, u, tasks, units);
     if (threadIdx.x == 0) at_s = c;
   }
   __syncthreads();
-  const Place c = at_s;
+  Place c = at_s;
+  c.h += wave.head0;
   if (c.block == 0) return;
   const ChunkTask t = p.tasks[c.task];
   const long long t0 = u - c.block;                      // the task's first unit
   const int c0 = (int)(t0 / share), c1 = (int)((t0 + t.blocks - 1) / share);
-  if (c0 != (int)blockIdx.x) return;
+  if (c0 != cta) return;
   const bool one = t.ntok <= p.tok_tile;
   const int np = (c1 - c0 + 1) * (one ? 2 : 1);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -798,7 +846,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   // partial i: slot of its CTA, and its row there
   auto slot = [&](int i) {
     const int k = one ? i >> 1 : i;
-    return k == 0 ? 2 * c0 + (t0 == c0 * share ? 0 : 1) : 2 * (c0 + k);
+    return 2 * (wi * p.ctas + c0 + k) + (k == 0 && t0 != c0 * share ? 1 : 0);
   };
   auto srow = [&](int i) { return one ? r + kTile * (i & 1) : row; };
   float M = -INFINITY, L = 0.f;
@@ -841,7 +889,7 @@ cudaError_t launch_d(const ChunkParams& p, cudaStream_t stream) {
   e = launch_pdl(chunk_kernel<D>, dim3((unsigned)p.ctas), dim3(kThreads), (size_t)Geo<D>::SMEM, stream, p);
   if (e != cudaSuccess || p.ctas == 1) return e;
   const int rows = p.n_new > p.tok_tile ? 2 * kTile : kTile;
-  return launch_pdl(merge_kernel<D>, dim3((unsigned)(p.ctas - 1), (unsigned)(rows / kMergeRows)), dim3(kMergeThreads), 0, stream, p);
+  return launch_pdl(merge_kernel<D>, dim3((unsigned)((p.ctas - 1) * p.waves_max), (unsigned)(rows / kMergeRows)), dim3(kMergeThreads), 0, stream, p);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -852,11 +900,13 @@ void plan_chunk(ChunkParams& p) {
   p.tok_tile = kTile / p.G;
   p.slots = p.n_new / (2 * p.tok_tile) + p.B;
   p.rows_cap = 2 * kTile;
+  // More than one wave only where some sequence can have several tasks.
+  p.waves_max = p.n_new > 2 * p.tok_tile ? (p.Hkv < kChunkMaxWaves ? p.Hkv : kChunkMaxWaves) : 1;
 }
 
 size_t chunk_workspace_bytes(const ChunkParams& p) {
   return up256((size_t)(p.slots + 1) * sizeof(ChunkTask)) +
-         (size_t)2 * kChunkMaxCtas * p.rows_cap * (sizeof(float2) + (size_t)p.d * 4);
+         (size_t)2 * kChunkMaxCtas * p.waves_max * p.rows_cap * (sizeof(float2) + (size_t)p.d * 4);
 }
 
 void bind_chunk(ChunkParams& p, void* scratch) {
@@ -864,7 +914,7 @@ void bind_chunk(ChunkParams& p, void* scratch) {
   p.tasks = reinterpret_cast<ChunkTask*>(w);
   w += up256((size_t)(p.slots + 1) * sizeof(ChunkTask));
   p.ml = reinterpret_cast<float2*>(w);
-  w += (size_t)2 * kChunkMaxCtas * p.rows_cap * sizeof(float2);
+  w += (size_t)2 * kChunkMaxCtas * p.waves_max * p.rows_cap * sizeof(float2);
   p.part = reinterpret_cast<float*>(w);
 }
 

@@ -152,17 +152,19 @@ struct ChunkParams {
   __nv_bfloat16* out;          // [n_new][Hq][d]
   float* lse;                  // [n_new][Hq] or null
   uint32_t* err;
-  ChunkTask* tasks;            // workspace: [slots] then the total of the units in tasks[slots].unit0
-  float* part;                 // workspace: [2 * ctas][d / 4][rows_cap] float4
-  float2* ml;                  // workspace: [2 * ctas][rows_cap] (running maximum, sum)
+  ChunkTask* tasks;            // workspace: [slots], then {b: tasks, tok0: waves, unit0: units of one KV head}
+  float* part;                 // workspace: [waves][ctas][2][d / 4][rows_cap] float4
+  float2* ml;                  // workspace: [waves][ctas][2][rows_cap] (running maximum, sum)
   int B, Hq, Hkv, G, d, cap, max_pages, num_pages, paged, n_new;
   int window, sinks;
   int slots, tok_tile;         // task slots; tokens per 128-row tile
   int rows_cap;                // rows of a partial
+  int waves_max;               // waves the workspace holds partials for
   int ctas;                    // CTAs that share the units
   int row_end;                 // rows of the K / V tensor maps (a box there reads zeros)
   float scale_log2;            // sigma * log2(e)
 };
+constexpr int kChunkMaxWaves = 4;
 constexpr int kChunkMaxCtas = 160;   // CTAs the chunk and window workspaces hold partials for
 void plan_chunk(ChunkParams& p);
 size_t chunk_workspace_bytes(const ChunkParams& p);
