@@ -10,7 +10,7 @@
 //   two tiles  a unit is one block of 128 keys, read once for both tiles;
 //   one tile   a unit is two blocks; each warpgroup takes one, with its own statistics and output
 //              (drafted tokens and short chunks: the cache is read at twice the rate per step).
-// A share that holds part of a task leaves a partial (m, l, O); merge_kernel joins those in order.
+// A share that holds part of a task leaves a partial (m, l, O); join_kernel puts those together in order.
 //
 // CTA: two softmax warpgroups (a thread is a row), one thread that issues the matrix
 // instructions, one warp that loads.  S = Q K^T goes to tensor memory; the softmax threads read
@@ -28,9 +28,9 @@ namespace {
 constexpr int kPage = 64;
 constexpr int kThreads = 384;      // 8 softmax warps, 1 matrix warp, 1 load warp, 2 idle: three warpgroups
 constexpr int kPlanThreads = 1024;
+constexpr int kOwnPlanSlots = 256;   // up to so many task slots every CTA makes the list itself
 constexpr int kTile = 128;
-constexpr int kMergeRows = 32;
-constexpr int kMergeThreads = 256;
+constexpr int kRowsCap = 2 * kTile;  // rows of a partial
 constexpr long long kLiveBytes = 48LL << 20;
 constexpr int kWaveUnits = 24;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -159,16 +159,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // again as 2 x 128 x 208 + 128 x 88.
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
-// Not to be moved out of the branch that needs it: most blocks are visible whole.
-__device__ __forceinline__ void hide_unless(float& x, uint32_t bit) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tselp.f32 %0, %0, 0fFF800000, p;\n\t}" : "+f"(x) : "r"(bit));
-}
 // Bits 0 .. x-1 of a 64-row page.
 __device__ __forceinline__ uint64_t low_bits(int x) { return x <= 0 ? 0ull : (x >= 64 ? ~0ull : (1ull << x) - 1); }
 
 // ----------------------------------------------------------------------------- plan
-template <typename T>
-__device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {  // inclusive, kPlanThreads threads
+template <int THREADS, typename T>
+__device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {  // inclusive
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -179,7 +175,7 @@ __device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {  // inclus
   __syncthreads();
   T before = 0;
   total = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
@@ -187,19 +183,22 @@ __device__ __forceinline__ T block_scan(T x, T* warp_sum, T& total) {  // inclus
   return x + before;
 }
 
+template <int THREADS>
+struct PlanSmem {
+  unsigned long long keys;  // rows that the chunks see, one KV head
+  long long lsum[THREADS / 32];
+  int sum[THREADS / 32], off[THREADS + 1];
+};
 // Tasks of every sequence, and the units before each: tasks[slots] holds their number and total.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ ChunkParams p) {
-  __shared__ int off_s[kPlanThreads + 1], sum_s[kPlanThreads / 32];
-  __shared__ long long lsum_s[kPlanThreads / 32];
-  pdl_wait();
-  pdl_trigger();
+// A whole CTA; its other threads see the tasks after a barrier.
+template <int THREADS>
+__device__ __forceinline__ void make_plan(const ChunkParams& p, ChunkTask* tasks, PlanSmem<THREADS>& S) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int span = 2 * p.tok_tile;
   int base = 0;
-  __shared__ unsigned long long keys_s;  // rows that the chunks see, one KV head
-  if (tid == 0) keys_s = 0;
+  if (tid == 0) S.keys = 0;
   __syncthreads();
-  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += THREADS) {
     const int b = b0 + tid;
     int cnt = 0;
     if (b < p.B) {
@@ -209,20 +208,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       else cnt = (s1 - s0 + span - 1) / span;
     }
     int total;
-    int end = block_scan(cnt, sum_s, total);
+    int end = block_scan<THREADS>(cnt, S.sum, total);
     // sequences that overlap could exceed the slots: such a sequence is skipped
     if (base + end > p.slots && cnt > 0) {
       record_error(p.err, kDevBadChunk, (uint32_t)b);
       end = p.slots - base;
     }
-    if (tid == 0) off_s[0] = 0;
-    off_s[tid + 1] = min(end, p.slots - base);
+    if (tid == 0) S.off[0] = 0;
+    S.off[tid + 1] = min(end, p.slots - base);
     __syncthreads();
-    for (int i = warp; i < min(kPlanThreads, p.B - b0); i += kPlanThreads / 32) {
-      const int k0 = off_s[i], k1 = off_s[i + 1];
+    for (int i = warp; i < min(THREADS, p.B - b0); i += THREADS / 32) {
+      const int k0 = S.off[i], k1 = S.off[i + 1];
       if (k0 >= k1) continue;
       const int s0 = p.q_start[b0 + i], T = p.q_start[b0 + i + 1] - s0, n = p.seqlens[b0 + i];
-      if (lane == 0) atomicAdd(&keys_s, (unsigned long long)visible_pages(n - T, n - 1, p.window, p.sinks).nv * kPage);
+      if (lane == 0) atomicAdd(&S.keys, (unsigned long long)visible_pages(n - T, n - 1, p.window, p.sinks).nv * kPage);
       for (int k = k0 + lane; k < k1; k += 32) {
         const int at = (k - k0) * span;
         ChunkTask t;
@@ -234,19 +233,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const int nv = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks).nv;
         t.blocks = t.ntok > p.tok_tile ? (nv + 1) >> 1 : (nv + 3) >> 2;
         t.seqlen = n;
-        p.tasks[base + k] = t;
+        tasks[base + k] = t;
       }
     }
     __syncthreads();
     base = min(base + total, p.slots);
   }
   long long units = 0;
-  for (int k0 = 0; k0 < base; k0 += kPlanThreads) {
+  for (int k0 = 0; k0 < base; k0 += THREADS) {
     const int k = k0 + tid;
-    const long long x = k < base ? p.tasks[k].blocks : 0;
+    const long long x = k < base ? tasks[k].blocks : 0;
     long long total;
-    const long long end = block_scan(x, lsum_s, total);
-    if (k < base) p.tasks[k].unit0 = units + end - x;
+    const long long end = block_scan<THREADS>(x, S.lsum, total);
+    if (k < base) tasks[k].unit0 = units + end - x;
     units += total;
   }
   if (tid == 0) {
@@ -254,14 +253,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     t.b = base;
     // Waves of at most kLiveBytes of K and V, where the blocks are read more than once and a
     // CTA's share of a wave stays long against the cost of a partial.
-    const long long once = (long long)keys_s * p.d * 4 * p.Hkv, block = (long long)kTile * p.d * 4;
+    const long long once = (long long)S.keys * p.d * 4 * p.Hkv, block = (long long)kTile * p.d * 4;
     int waves = 1;
     if (units * p.Hkv * block > once + once / 2)
       while (waves < p.waves_max && once > waves * kLiveBytes && units * p.Hkv > (long long)(waves + 1) * p.ctas * kWaveUnits) ++waves;
     t.tok0 = waves;
     t.unit0 = units;
-    p.tasks[p.slots] = t;
+    tasks[p.slots] = t;
   }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ PlanSmem<kPlanThreads> S;
+  pdl_wait();
+  pdl_trigger();
+  make_plan<kPlanThreads>(p, p.tasks, S);
 }
 
 // ----------------------------------------------------------------------------- shares
@@ -286,7 +292,7 @@ __device__ __forceinline__ Wave wave_of(const ChunkParams& p, int w, int waves, 
   return x;
 }
 // Task, KV head and unit of the task at global unit u; whole warp.
-__device__ __forceinline__ Place find_unit(const ChunkParams& p, long long u, int tasks, long long units) {
+__device__ __forceinline__ Place find_unit(const ChunkTask* list, long long u, int tasks, long long units) {
   const int lane = threadIdx.x & 31;
   Place c;
   c.h = (int)(u / units);
@@ -294,13 +300,13 @@ __device__ __forceinline__ Place find_unit(const ChunkParams& p, long long u, in
   int lo = 0, cnt = tasks;
   while (cnt > 1) {
     const int step = (cnt + 31) / 32;
-    const bool in = lane * step < cnt && p.tasks[lo + lane * step].unit0 <= rem;
+    const bool in = lane * step < cnt && list[lo + lane * step].unit0 <= rem;
     const int k = __popc(__ballot_sync(0xffffffffu, in)) - 1;
     lo += k * step;
     cnt = min(step, cnt - k * step);
   }
   c.task = lo;
-  c.block = (int)(rem - p.tasks[lo].unit0);
+  c.block = (int)(rem - list[lo].unit0);
   return c;
 }
 __device__ __forceinline__ void next_task(Place& c, int tasks) {
@@ -332,6 +338,39 @@ __device__ __forceinline__ int ring_v(bool one, int j, int x, int n) {
   return one ? (j + 1 < n ? 4 * j + 3 + 2 * x : 4 * j + 2 + x) : (j + 1 < n ? 2 * j + 2 : 2 * j + 1);
 }
 
+// What a softmax warpgroup knows of a segment.  Made anew where it is needed, from the list that a
+// shared variable points to: kept over the loop on the blocks it would push the scores out of registers.
+struct GroupSeg {
+  ChunkTask t;
+  VisiblePages vis;
+  bool one;
+  int tile, toks, plo, phi, block;
+  __device__ __forceinline__ GroupSeg(const ChunkParams& p, const ChunkTask* const volatile& list, const Place& c, int x) {
+    t = list[c.task];
+    one = t.ntok <= p.tok_tile;
+    vis = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks);
+    tile = one ? 0 : x;
+    toks = min(p.tok_tile, t.ntok - tile * p.tok_tile);
+    plo = t.pos0 + tile * p.tok_tile;
+    phi = plo + toks - 1;
+    block = c.block;
+  }
+  // Blocks a .. b - 1 of the segment lie inside the window of every row, whole: pages from pg0 to
+  // pg1 - 1 of the sequence, behind the sinks' pages of the list.
+  __device__ __forceinline__ void plain(const ChunkParams& p, int x, int& a, int& b) const {
+    const int pg0 = max(vis.w0, p.window > 0 ? (max(0, phi - p.window + 1) + kPage - 1) / kPage : 0);
+    const int pg1 = (plo + 1) / kPage;
+    const int a0 = pg0 - vis.w0 + vis.ns, a1 = pg1 - vis.w0 + vis.ns;  // in the list
+    if (one) {
+      a = ((a0 - 2 * x + 3) >> 2) - block;
+      b = ((a1 - 2 * x + 2) >> 2) - block;
+    } else {
+      a = ((a0 + 1) >> 1) - block;
+      b = (a1 >> 1) - block;
+    }
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
   using Gm = Geo<D>;
@@ -342,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   __shared__ uint64_t full[ST], empty[ST], q_full, q_empty, s_full[2], s_read[2], p_ready[2], pv_done[2], half_full, half_free, drain;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int stop_s;
+  __shared__ const ChunkTask* volatile list_s;
   __shared__ Share share_s[kChunkMaxWaves];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
@@ -370,15 +410,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   }
   pdl_wait();
   pdl_trigger();
-  const int tasks = p.tasks[p.slots].b;
-  const long long units = p.tasks[p.slots].unit0;
-  const int waves = p.tasks[p.slots].tok0;
+  // Few tasks: every CTA makes the list for itself, which costs less than a kernel before this one.
+  const ChunkTask* list = p.tasks;
+  if (p.own_plan) {
+    ChunkTask* own = p.tasks + (size_t)blockIdx.x * (p.slots + 1);
+    make_plan<kThreads>(p, own, *reinterpret_cast<PlanSmem<kThreads>*>(ring));
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies write there next
+    __syncthreads();
+    list = own;
+  }
+  if (tid == 0) list_s = list;
+  const int tasks = list[p.slots].b;
+  const long long units = list[p.slots].unit0;
+  const int waves = list[p.slots].tok0;
   if (warp < waves) {
     const Wave w = wave_of(p, warp, waves, units);
     Share x;
     x.u0 = min(w.share * blockIdx.x, w.total);
     x.u1 = min(x.u0 + w.share, w.total);
-    if (x.u0 < x.u1) x.at = find_unit(p, x.u0, tasks, units);
+    if (x.u0 < x.u1) x.at = find_unit(list, x.u0, tasks, units);
     x.at.h += w.head0;
     if (lane == 0) share_s[warp] = x;
   }
@@ -396,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     Place c = share_s[w].at;
     const long long u1 = share_s[w].u1;
     for (long long u = share_s[w].u0; u < u1 && live;) {
-      const ChunkTask t = p.tasks[c.task];
+      const ChunkTask t = list[c.task];
       const int be = (int)min((long long)t.blocks, c.block + (u1 - u)), units_here = be - c.block;
       const bool one = t.ntok <= p.tok_tile;
       const VisiblePages vis = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks);
@@ -508,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       Place c = share_s[w].at;
       const long long u1 = share_s[w].u1;
       for (long long u = share_s[w].u0; u < u1 && live; ++seg) {
-        const ChunkTask t = p.tasks[c.task];
+        const ChunkTask t = list[c.task];
         const int n = (int)min((long long)t.blocks - c.block, u1 - u);
         const bool one = t.ntok <= p.tok_tile;
         live = wait_warp(&q_full, seg & 1, &stop_s);
@@ -565,242 +615,244 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     bool half_used = false;
     // After a wait that ran out the waits below return at once and what is computed does not count.
     for (int w = 0; w < waves; ++w) {
-    Place c = share_s[w].at;
-    const long long u0 = share_s[w].u0, u1 = share_s[w].u1;
-    for (long long u = u0; u < u1;) {
-      const ChunkTask t = p.tasks[c.task];
-      const int n_seq = t.seqlen;
-      const int n = (int)min((long long)t.blocks - c.block, u1 - u);
-      const bool one = t.ntok <= p.tok_tile;
-      const VisiblePages vis = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks);
-      const int tile = one ? 0 : x;
-      const int toks = min(p.tok_tile, t.ntok - tile * p.tok_tile);
-      const int plo = t.pos0 + tile * p.tok_tile, phi = plo + toks - 1;
-      const bool mine = r < toks * p.G, busy = quad * 32 < toks * p.G;
-      const int tok = r / p.G, pos = plo + tok;
-      const int wlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;  // first of the row's window
-      float m = -INFINITY, l = 0.f;
-      // Blocks plain0 .. plain1 - 1 of the segment lie inside the window of every row, whole: pages
-      // from pg0 to pg1 - 1 of the sequence, behind the sinks' pages of the list.
-      int plain0, plain1;
-      {
-        const int pg0 = max(vis.w0, p.window > 0 ? (max(0, phi - p.window + 1) + kPage - 1) / kPage : 0);
-        const int pg1 = (plo + 1) / kPage;
-        const int a0 = pg0 - vis.w0 + vis.ns, a1 = pg1 - vis.w0 + vis.ns;  // in the list
-        if (one) {
-          plain0 = ((a0 - 2 * x + 3) >> 2) - c.block;
-          plain1 = ((a1 - 2 * x + 2) >> 2) - c.block;
+      Place c = share_s[w].at;
+      long long left = share_s[w].u1 - share_s[w].u0;
+      bool first = true;
+      while (left > 0) {
+        int n, plain0, plain1;
+        bool one, mine, busy;
+        {
+          const GroupSeg g(p, list_s, c, x);
+          n = (int)min((long long)g.t.blocks - c.block, left);
+          one = g.one;
+          mine = r < g.toks * p.G;
+          busy = quad * 32 < g.toks * p.G;
+          g.plain(p, x, plain0, plain1);
+        }
+        float m = -INFINITY, l = 0.f;
+
+        // V rows that no token sees may hold anything, and 0 * NaN is not 0: a thread clears its row.
+        auto clear_row = [&](int j) {
+          const GroupSeg g(p, list_s, c, x);
+          const int v = (one ? (c.block + j) * 4 + 2 * x : (c.block + j) * 2) + (r >> 6);
+          const int pj = g.vis.page(v) * kPage + (r & 63);
+          const bool clear = v < g.vis.nv && (pj >= g.t.seqlen || (pj < g.vis.first && pj >= p.sinks));
+          if (__any_sync(0xffffffffu, clear)) {
+            const int idx = base + ring_v(one, j, x, n), st = idx % ST;
+            wait_row(&full[st], (idx / ST) & 1, &stop_s);
+            if (clear) {
+              unsigned char* z = ring + (size_t)st * Gm::TILE_BYTES + r * 128;
+#pragma unroll
+              for (int hf = 0; hf < Gm::HALVES; ++hf)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(z + hf * Gm::HALF_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncwarp();
+          }
+        };
+
+        if (!busy) {  // a warp without rows keeps step
+          for (int j = 0; j < n; ++j) {
+            wait_row(&s_full[x], ph_s, &stop_s);
+            ph_s ^= 1;
+            if (j < plain0 || j >= plain1) clear_row(j);
+            if (lane == 0) mbar_arrive(&s_read[s_buf]);
+            if (j > 0) {
+              wait_row(&pv_done[x], ph_o, &stop_s);
+              ph_o ^= 1;
+            }
+            if (lane == 0) mbar_arrive(&p_ready[x]);
+          }
         } else {
-          plain0 = ((a0 + 1) >> 1) - c.block;
-          plain1 = (a1 >> 1) - c.block;
-        }
-      }
-
-      for (int j = 0; j < n; ++j) {
-        const int v0 = one ? (c.block + j) * 4 + 2 * x : (c.block + j) * 2;
-        bool whole = true, dirty = false;
-        int at[2] = {0, 0};
-        if (j < plain0 || j >= plain1) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int j0 = vis.page(v0 + i) * kPage;
-            at[i] = v0 + i < vis.nv ? j0 : -1;
-            if (v0 + i >= vis.nv) {
-              whole = false;
-            } else {
-              whole = whole && j0 + kPage - 1 <= plo && (p.window <= 0 || j0 > phi - p.window || j0 + kPage <= p.sinks);
-              // rows that no token sees may hold anything, and 0 * NaN is not 0
-              dirty = dirty || j0 + kPage > n_seq || (j0 < vis.first && j0 + kPage > p.sinks);
-            }
-          }
-        }
-        wait_row(&s_full[x], ph_s, &stop_s);
-        ph_s ^= 1;
-        tc_fence_after();
-        float s[kTile];
-        if (busy) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s + 32 * i, tS + 32 * i);
-          tmem_wait_ld();
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_read[s_buf]);
-        bool grow = false;
-        float f = 1.f;
-        if (busy) {
-          if (!whole) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint64_t see = 0;
-              if (mine && at[i] >= 0)
-                see = low_bits(pos + 1 - at[i]) & (~low_bits(wlo - at[i]) | low_bits(p.sinks - at[i]));
-              const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                hide_unless(s[64 * i + e], lo & (1u << e));
-                hide_unless(s[64 * i + 32 + e], hi & (1u << e));
-              }
-            }
-          }
-          float mx[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mx[e] = max3(s[e], s[8 + e], s[16 + e]);
-#pragma unroll
-          for (int i = 24; i < kTile - 8; i += 16)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 8 + e]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mx[e] = fmaxf(mx[e], s[kTile - 8 + e]);
-          const float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[4]), max3(mx[5], mx[6], mx[7]));
-          grow = __any_sync(0xffffffffu, mine && top > m + grow_by);
-          if (grow) {
-            const float mn = fmaxf(m, top);
-            f = m == -INFINITY ? 0.f : ex2((m - mn) * scale);
-            l *= f;
-            m = mn;
-          }
-        }
-        // The product of the block before has read P, and O may be scaled.
-        if (j > 0) {
-          wait_row(&pv_done[x], ph_o, &stop_s);
-          ph_o ^= 1;
-          tc_fence_after();
-        }
-        if (dirty) {
-          const int idx = base + ring_v(one, j, x, n), st = idx % ST;
-          wait_row(&full[st], (idx / ST) & 1, &stop_s);
-          const int a = r < 64 ? at[0] : at[1], pj = a + (r & 63);
-          if (a >= 0 && (pj >= n_seq || (pj < vis.first && pj >= p.sinks))) {
-            unsigned char* z = ring + (size_t)st * Gm::TILE_BYTES + r * 128;
-#pragma unroll
-            for (int hf = 0; hf < Gm::HALVES; ++hf)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(z + hf * Gm::HALF_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        if (busy) {
-          if (grow && j > 0) {
+          // The loop is kept to one straight run of instructions with few branches over rare work:
+          // with a branch around each part of it for warps without rows it took 386K cycles instead
+          // of 344K for 512 tokens on 32K rows.
+          for (int j = 0; j < n; ++j) {
+            wait_row(&s_full[x], ph_s, &stop_s);
+            ph_s ^= 1;
+            tc_fence_after();
+            if (j < plain0 || j >= plain1) {
+              // Scores that a row does not see are overwritten where they lie, 8 at a time.
+              clear_row(j);
+              const GroupSeg g(p, list_s, c, x);
+              const int pos = g.plo + r / p.G, wlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
 #pragma unroll 1
-            for (int i = 0; i < D / 8; ++i) {  // 8 columns at a time: the scores stay in registers
-              float o[8];
-              tmem_ld8(o, tO + 8 * i);
-              tmem_wait_ld();
+              for (int i = 0; i < 2; ++i) {
+                const int v = (one ? (c.block + j) * 4 + 2 * x : (c.block + j) * 2) + i, j0 = g.vis.page(v) * kPage;
+                uint64_t see = ~0ull;
+                if (mine)
+                  see = v < g.vis.nv ? low_bits(pos + 1 - j0) & (~low_bits(wlo - j0) | low_bits(p.sinks - j0)) : 0;
+                if (__all_sync(0xffffffffu, see == ~0ull)) continue;
+#pragma unroll 1
+                for (int k = 0; k < kPage; k += 8, see >>= 8) {
+                  float y[8];
+                  tmem_ld8(y, tS + i * kPage + k);
+                  tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] *= f;
-              tmem_st8(tO + 8 * i, o);
+                  for (int e = 0; e < 8; ++e)
+                    if (!((uint32_t)see & (1u << e))) y[e] = -INFINITY;
+                  tmem_st8(tS + i * kPage + k, y);
+                }
+              }
+              tmem_wait_st();
             }
-          }
-          const float off = m == -INFINITY ? 0.f : -m * scale;
-          const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
-          float2 sum[4];
+            float s[kTile];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 z = ffma2(make_float2(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), sc2, off2);
-              z.x = ex2(z.x);
-              z.y = ex2(z.y);
-              sum[e & 3] = __fadd2_rn(sum[e & 3], z);
-              w[e] = pack_bf16(z.x, z.y);
-            }
-            tmem_st16(tP + 16 * i, w);
-          }
-          sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-          l += sum[0].x + sum[0].y;
-        }
-        if (busy) tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[x]);
-      }
-
-      // ---- this segment's rows ----
-      wait_row(&pv_done[x], ph_o, &stop_s);
-      ph_o ^= 1;
-      tc_fence_after();
-      const bool done = n == t.blocks;
-      const int slot = 2 * (w * p.ctas + (int)blockIdx.x) + (u == u0 ? 0 : 1);
-      float4* part = reinterpret_cast<float4*>(p.part) + (size_t)slot * (D / 4) * p.rows_cap;
-      float2* ml = p.ml + (size_t)slot * p.rows_cap;
-      const float mz = m == -INFINITY ? m : m * scale;
-      if (!done || (one && x == 1)) {
-        if (done && half_used) {  // the other warpgroup has read the half it got before
-          wait_row(&half_free, ph_half ^ 1, &stop_s);
-        }
-        if (busy) {
-          const int at = x * kTile + r;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            float o[32];
-            tmem_ld32(o, tO + 32 * i);
+            for (int i = 0; i < 4; ++i) tmem_ld32(s + 32 * i, tS + 32 * i);
             tmem_wait_ld();
-            if (mine)
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_read[s_buf]);
+            float mx[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                part[(size_t)(8 * i + e) * p.rows_cap + at] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-          if (mine) ml[at] = make_float2(mz, l);
-        }
-        if (done) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&half_full);
-          half_used = true;
-          ph_half ^= 1;
-        }
-      } else {
-        float f0 = 1.f, f1 = 0.f, M = mz, L = l;
-        if (one) {
-          wait_row(&half_full, ph_half, &stop_s);
-          ph_half ^= 1;
-          if (mine) {
-            const float2 y = __ldcg(ml + kTile + r);
-            M = fmaxf(mz, y.x);
-            f0 = mz == -INFINITY ? 0.f : ex2(mz - M);
-            f1 = y.x == -INFINITY ? 0.f : ex2(y.x - M);
-            L = l * f0 + y.y * f1;
-          }
-        }
-        if (busy) {
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-          const size_t o_row = (size_t)(t.tok0 + tile * p.tok_tile + tok) * p.Hq + c.h * p.G + r % p.G;
-          uint4* dst = reinterpret_cast<uint4*>(p.out + o_row * D);
+            for (int e = 0; e < 8; ++e) mx[e] = max3(s[e], s[8 + e], s[16 + e]);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            float o[32];
-            tmem_ld32(o, tO + 32 * i);
-            tmem_wait_ld();
-            if (!mine) continue;
-            if (one) {
+            for (int i = 24; i < kTile - 8; i += 16)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 y = __ldcg(part + (size_t)(8 * i + e) * p.rows_cap + kTile + r);
-                o[4 * e] = o[4 * e] * f0 + y.x * f1;
-                o[4 * e + 1] = o[4 * e + 1] * f0 + y.y * f1;
-                o[4 * e + 2] = o[4 * e + 2] * f0 + y.z * f1;
-                o[4 * e + 3] = o[4 * e + 3] * f0 + y.w * f1;
+              for (int e = 0; e < 8; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 8 + e]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx[e] = fmaxf(mx[e], s[kTile - 8 + e]);
+            const float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[4]), max3(mx[5], mx[6], mx[7]));
+            const bool grow = __any_sync(0xffffffffu, mine && top > m + grow_by);
+            const float mn = grow ? fmaxf(m, top) : m;
+            const float f = m == -INFINITY ? 0.f : ex2((m - mn) * scale);  // 1 where m stays
+            m = mn;
+            // The product of the block before has read P, and O may be scaled.
+            if (j > 0) {
+              wait_row(&pv_done[x], ph_o, &stop_s);
+              ph_o ^= 1;
+              tc_fence_after();
+              if (grow) {
+#pragma unroll 1
+                for (int i = 0; i < D / 8; ++i) {  // 8 columns at a time: the scores stay in registers
+                  float o[8];
+                  tmem_ld8(o, tO + 8 * i);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) o[e] *= f;
+                  tmem_st8(tO + 8 * i, o);
+                }
               }
             }
+            const float off = m == -INFINITY ? 0.f : -m * scale;
+            const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
+            float2 sum[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[4 * i + e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                          pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t q[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float2 z = ffma2(make_float2(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), sc2, off2);
+                z.x = ex2(z.x);
+                z.y = ex2(z.y);
+                sum[e & 3] = __fadd2_rn(sum[e & 3], z);
+                q[e] = pack_bf16(z.x, z.y);
+              }
+              tmem_st16(tP + 16 * i, q);
+            }
+            sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+            l = l * f + (sum[0].x + sum[0].y);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[x]);
           }
-          if (mine && p.lse != nullptr) p.lse[o_row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
         }
-        if (one) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&half_free);
+
+        // ---- this segment's rows ----
+        wait_row(&pv_done[x], ph_o, &stop_s);
+        ph_o ^= 1;
+        tc_fence_after();
+        const GroupSeg g(p, list_s, c, x);
+        const bool done = n == g.t.blocks;
+        const int slot = 2 * (w * p.ctas + (int)blockIdx.x) + (first ? 0 : 1);
+        float4* part = reinterpret_cast<float4*>(p.part) + (size_t)slot * (D / 4) * kRowsCap;
+        float2* ml = p.ml + (size_t)slot * kRowsCap;
+        const float mz = m == -INFINITY ? m : m * scale;
+        if (!done || (one && x == 1)) {
+          // the other warpgroup has read the half it got before
+          if (done && half_used) wait_row(&half_free, ph_half ^ 1, &stop_s);
+          if (busy) {
+            const int at = x * kTile + r;
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              float o[32];
+              tmem_ld32(o, tO + 32 * i);
+              tmem_wait_ld();
+              if (mine) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  part[(size_t)(8 * i + e) * kRowsCap + at] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              }
+              __syncwarp();
+            }
+            if (mine) ml[at] = make_float2(mz, l);
+          }
+          if (done) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&half_full);
+            half_used = true;
+            ph_half ^= 1;
+          }
+        } else {
+          float f0 = 1.f, f1 = 0.f, M = mz, L = l;
+          if (one) {
+            wait_row(&half_full, ph_half, &stop_s);
+            ph_half ^= 1;
+            if (mine) {
+              const float2 y = __ldcg(ml + kTile + r);
+              M = fmaxf(mz, y.x);
+              f0 = mz == -INFINITY ? 0.f : ex2(mz - M);
+              f1 = y.x == -INFINITY ? 0.f : ex2(y.x - M);
+              L = l * f0 + y.y * f1;
+            }
+          }
+          if (busy) {
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const size_t o_row = (size_t)(g.t.tok0 + g.tile * p.tok_tile + r / p.G) * p.Hq + c.h * p.G + r % p.G;
+            uint4* dst = reinterpret_cast<uint4*>(p.out + o_row * D);
+            f0 *= inv;
+            f1 *= inv;
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              float o[32];
+              tmem_ld32(o, tO + 32 * i);
+              tmem_wait_ld();
+              if (mine) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= f0;
+                if (one) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    const float4 y = __ldcg(part + (size_t)(8 * i + e) * kRowsCap + kTile + r);
+                    o[4 * e] += y.x * f1;
+                    o[4 * e + 1] += y.y * f1;
+                    o[4 * e + 2] += y.z * f1;
+                    o[4 * e + 3] += y.w * f1;
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  dst[4 * i + e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                              pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+              }
+              __syncwarp();
+            }
+            if (mine && p.lse != nullptr) p.lse[o_row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+          }
+          if (one) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&half_free);
+          }
         }
+        base += (one ? 4 : 2) * n;
+        left -= n;
+        first = false;
+        next_task(c, tasks);
       }
-      base += (one ? 4 : 2) * n;
-      u += n;
-      next_task(c, tasks);
-    }
     }
     tc_fence_before();
   }
@@ -810,10 +862,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   if (tid == 0 && stop_s) record_error(p.err, kDevWaitTimeout, blockIdx.x);
 }
 
-// Joins the partials of a task that several CTAs share, in CTA order.  blockIdx.x names
-// the wave and the share whose beginning is looked at: the first one inside a task acts for it, 32 rows a CTA.
+// Joins the partials of a task that several CTAs share, in CTA order.  blockIdx.x names the wave and
+// the share whose beginning is looked at: the first one inside a task acts for it.  (A join by the
+// last CTA of the task, in the kernel above, has too few loads in flight: 512 tokens on 32K rows
+// took 499 us with it, 287 us with a kernel of its own.)
+constexpr int kJoinThreads = 1024;
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ ChunkParams p) {
   __shared__ Place at_s;
   pdl_wait();
   pdl_trigger();
@@ -825,7 +880,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   const long long share = wave.share, u = share * (cta + 1);
   if (u >= wave.total) return;
   if (threadIdx.x < 32) {
-    const Place c = find_unit(p, u, tasks, units);
+    const Place c = find_unit(p.tasks, u, tasks, units);
     if (threadIdx.x == 0) at_s = c;
   }
   __syncthreads();
@@ -837,84 +892,97 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   const int c0 = (int)(t0 / share), c1 = (int)((t0 + t.blocks - 1) / share);
   if (c0 != cta) return;
   const bool one = t.ntok <= p.tok_tile;
-  const int np = (c1 - c0 + 1) * (one ? 2 : 1);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.y * kMergeRows + lane;        // row of the task's 256
-  const int tile = row / kTile, r = row % kTile;
-  const int toks = min(p.tok_tile, t.ntok - tile * p.tok_tile);
-  if (r >= toks * p.G) return;
-  // partial i: slot of its CTA, and its row there
-  auto slot = [&](int i) {
-    const int k = one ? i >> 1 : i;
-    return 2 * (wi * p.ctas + c0 + k) + (k == 0 && t0 != c0 * share ? 1 : 0);
-  };
-  auto srow = [&](int i) { return one ? r + kTile * (i & 1) : row; };
-  float M = -INFINITY, L = 0.f;
-  for (int i = 0; i < np; ++i) M = fmaxf(M, p.ml[(size_t)slot(i) * p.rows_cap + srow(i)].x);
-  constexpr int C4 = D / 4 / (kMergeThreads / 32);       // float4 columns per thread
-  float4 acc[C4];
-#pragma unroll
-  for (int e = 0; e < C4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int i = 0; i < np; ++i) {
-    const float2 y = p.ml[(size_t)slot(i) * p.rows_cap + srow(i)];
-    const float f = y.x == -INFINITY ? 0.f : ex2(y.x - M);
-    L += f * y.y;
-    const float4* part = reinterpret_cast<const float4*>(p.part) + (size_t)slot(i) * (D / 4) * p.rows_cap + srow(i);
-#pragma unroll
-    for (int e = 0; e < C4; ++e) {
-      const float4 o = __ldcg(part + (size_t)(warp * C4 + e) * p.rows_cap);
-      acc[e].x += f * o.x;
-      acc[e].y += f * o.y;
-      acc[e].z += f * o.z;
-      acc[e].w += f * o.w;
+  const int per = one ? 2 : 1, np = (c1 - c0 + 1) * per;
+  const int slot1 = 2 * (wi * p.ctas + c0), slot0 = slot1 + (t0 != c0 * share ? 1 : 0);
+  // Place of partial i of a row; a one-tile task has two per CTA, 128 rows apart.
+  auto slot = [&](int i) { return i < per ? slot0 : slot1 + 2 * (one ? i >> 1 : i); };
+  auto line = [&](int i, int row) { return one ? row + (i & 1) * kTile : row; };
+  auto token = [&](int row) { return (size_t)t.tok0 + (row / kTile) * p.tok_tile + row % kTile / p.G; };
+  auto valid = [&](int row) { return row % kTile < (min(p.tok_tile, t.ntok - row / kTile * p.tok_tile)) * p.G; };
+  if (threadIdx.x < kRowsCap && valid(threadIdx.x)) {
+    const int row = threadIdx.x;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) M = fmaxf(M, p.ml[(size_t)slot(i) * kRowsCap + line(i, row)].x);
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+      float2* y = p.ml + (size_t)slot(i) * kRowsCap + line(i, row);
+      const float f = y->x == -INFINITY ? 0.f : ex2(y->x - M);
+      L += f * y->y;
+      y->x = f;                                          // the partial's factor takes the place of its maximum
     }
+    const int tok_row = row % kTile % p.G;
+    // the sum's place in the first partial holds its inverse
+    p.ml[(size_t)slot0 * kRowsCap + row].y = L > 0.f ? 1.f / L : 0.f;
+    if (p.lse != nullptr) p.lse[token(row) * p.Hq + c.h * p.G + tok_row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  const size_t o_row = (size_t)(t.tok0 + tile * p.tok_tile + r / p.G) * p.Hq + c.h * p.G + r % p.G;
-  uint4* dst = reinterpret_cast<uint4*>(p.out + o_row * D + warp * C4 * 4);
-#pragma unroll
-  for (int e = 0; e < C4; e += 2)
-    dst[e / 2] = make_uint4(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv),
-                            pack_bf16(acc[e + 1].x * inv, acc[e + 1].y * inv), pack_bf16(acc[e + 1].z * inv, acc[e + 1].w * inv));
-  if (warp == 0 && p.lse != nullptr) p.lse[o_row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  __syncthreads();
+  // A warp takes 8 columns of 32 rows at a time.
+  const int lane = threadIdx.x & 31, groups = one ? (min(p.tok_tile, t.ntok) * p.G + 31) / 32 : kRowsCap / 32;
+  for (int e = threadIdx.x >> 5; e < groups * (D / 8); e += kJoinThreads / 32) {
+    const int row = e % groups * 32 + lane, c8 = e / groups;
+    if (!valid(row)) continue;
+    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+      const int at = line(i, row);
+      const float f = p.ml[(size_t)slot(i) * kRowsCap + at].x;
+      const float4* part = reinterpret_cast<const float4*>(p.part) + ((size_t)slot(i) * (D / 4) + 2 * c8) * kRowsCap + at;
+      const float4 o0 = __ldcg(part), o1 = __ldcg(part + kRowsCap);
+      a[0] += f * o0.x;
+      a[1] += f * o0.y;
+      a[2] += f * o0.z;
+      a[3] += f * o0.w;
+      a[4] += f * o1.x;
+      a[5] += f * o1.y;
+      a[6] += f * o1.z;
+      a[7] += f * o1.w;
+    }
+    const float inv = p.ml[(size_t)slot0 * kRowsCap + row].y;
+    reinterpret_cast<uint4*>(p.out + (token(row) * p.Hq + c.h * p.G + row % kTile % p.G) * D)[c8] =
+        make_uint4(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[2] * inv, a[3] * inv), pack_bf16(a[4] * inv, a[5] * inv),
+                   pack_bf16(a[6] * inv, a[7] * inv));
+  }
 }
 
 template <int D>
 cudaError_t launch_d(const ChunkParams& p, cudaStream_t stream) {
   cudaError_t e = prepare_kernel((const void*)chunk_kernel<D>, Geo<D>::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
-  if (e != cudaSuccess) return e;
+  if (!p.own_plan) {
+    e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_pdl(chunk_kernel<D>, dim3((unsigned)p.ctas), dim3(kThreads), (size_t)Geo<D>::SMEM, stream, p);
   if (e != cudaSuccess || p.ctas == 1) return e;
-  const int rows = p.n_new > p.tok_tile ? 2 * kTile : kTile;
-  return launch_pdl(merge_kernel<D>, dim3((unsigned)((p.ctas - 1) * p.waves_max), (unsigned)(rows / kMergeRows)), dim3(kMergeThreads), 0, stream, p);
+  return launch_pdl(join_kernel<D>, dim3((unsigned)((p.ctas - 1) * p.waves_max)), dim3(kJoinThreads), 0, stream, p);
 }
 
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+size_t task_bytes(const ChunkParams& p) {
+  return ((size_t)(p.own_plan ? kChunkMaxCtas : 1) * (p.slots + 1) * sizeof(ChunkTask) + 255) & ~(size_t)255;
+}
 
 }  // namespace
 
 void plan_chunk(ChunkParams& p) {
   p.tok_tile = kTile / p.G;
   p.slots = p.n_new / (2 * p.tok_tile) + p.B;
-  p.rows_cap = 2 * kTile;
+  p.own_plan = p.slots <= kOwnPlanSlots ? 1 : 0;
   // More than one wave only where some sequence can have several tasks.
   p.waves_max = p.n_new > 2 * p.tok_tile ? (p.Hkv < kChunkMaxWaves ? p.Hkv : kChunkMaxWaves) : 1;
 }
 
 size_t chunk_workspace_bytes(const ChunkParams& p) {
-  return up256((size_t)(p.slots + 1) * sizeof(ChunkTask)) +
-         (size_t)2 * kChunkMaxCtas * p.waves_max * p.rows_cap * (sizeof(float2) + (size_t)p.d * 4);
+  return task_bytes(p) +
+         (size_t)2 * kChunkMaxCtas * p.waves_max * kRowsCap * (sizeof(float2) + (size_t)p.d * 4);
 }
 
 void bind_chunk(ChunkParams& p, void* scratch) {
   unsigned char* w = static_cast<unsigned char*>(scratch);
   p.tasks = reinterpret_cast<ChunkTask*>(w);
-  w += up256((size_t)(p.slots + 1) * sizeof(ChunkTask));
+  w += task_bytes(p);
   p.ml = reinterpret_cast<float2*>(w);
-  w += (size_t)2 * kChunkMaxCtas * p.waves_max * p.rows_cap * sizeof(float2);
+  w += (size_t)2 * kChunkMaxCtas * p.waves_max * kRowsCap * sizeof(float2);
   p.part = reinterpret_cast<float*>(w);
 }
 

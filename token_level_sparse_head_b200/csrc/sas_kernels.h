@@ -153,12 +153,12 @@ struct ChunkParams {
   float* lse;                  // [n_new][Hq] or null
   uint32_t* err;
   ChunkTask* tasks;            // workspace: [slots], then {b: tasks, tok0: waves, unit0: units of one KV head}
-  float* part;                 // workspace: [waves][ctas][2][d / 4][rows_cap] float4
-  float2* ml;                  // workspace: [waves][ctas][2][rows_cap] (running maximum, sum)
+  float* part;                 // workspace: [waves][ctas][2][d / 4][256 rows] float4
+  float2* ml;                  // workspace: [waves][ctas][2][256 rows] (running maximum, sum)
   int B, Hq, Hkv, G, d, cap, max_pages, num_pages, paged, n_new;
   int window, sinks;
   int slots, tok_tile;         // task slots; tokens per 128-row tile
-  int rows_cap;                // rows of a partial
+  int own_plan;                // every CTA makes its own list of tasks, at tasks + CTA * (slots + 1)
   int waves_max;               // waves the workspace holds partials for
   int ctas;                    // CTAs that share the units
   int row_end;                 // rows of the K / V tensor maps (a box there reads zeros)
