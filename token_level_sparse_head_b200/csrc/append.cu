@@ -8,10 +8,15 @@
 //
 // Two kernels, by the number of (token, head) pairs:
 //   token_kernel  one CTA per pair, 8 threads per output: few tokens, where latency counts;
-//   tile_kernel   CTA = 64 tokens x one head.  K rows and M[h] are staged in shared memory, M
-//                 transposed to [channel][output] so that a thread takes 8 outputs of 2 tokens
-//                 with two 16-byte loads of M per channel, in paired fp32 FMAs (bit-identical to
+//   tile_kernel   tiles of 128 tokens x one head, shared by as many CTAs as are resident at once.
+//                 M[h] is staged in shared memory once per CTA, transposed to [channel][output];
+//                 a tile's keys come by asynchronous copies while the tile before is worked on.
+//                 A thread takes 4 outputs of 4 tokens in paired fp32 FMAs (bit-identical to
 //                 single ones).
+// What bounds the tiles: moving K and V of 8192 tokens and 8 heads (67 MB in and out) takes 9.6 us
+// alone, the call with 32 outputs per row 26 us: 268 M fp32 FMAs are 7.5 us at full rate, and the
+// conversions and loads of their operands as much again.  The tensor cores would need another
+// summation order, and rows would then depend on the call that wrote them.
 #include <cuda_fp8.h>
 
 #include "sas_device.cuh"
@@ -117,137 +122,158 @@ __global__ void __launch_bounds__(256) token_kernel(const AppendParams p) {
   }
 }
 
-constexpr int kTileTokens = 64;
-constexpr int kTileThreads = 128;
+constexpr int kTileTokens = 128;
+constexpr int kTileThreads = 256;
 
 template <int D, int R>
 struct TileSmem {
-  static constexpr int KPITCH = D * 2 + 16;  // bytes: rows of a pair of tokens start in other banks
+  static constexpr int KPITCH = D * 2 + 16;  // bytes: neighbouring rows start 4 banks apart
   float Mt[D][R];                            // M[h] transposed
-  unsigned char K[kTileTokens][KPITCH];
-  long long row[kTileTokens];
+  unsigned char K[2][kTileTokens][KPITCH];
+  long long row[2][kTileTokens];
 };
 
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <int D, int R, bool FP8>
-__global__ void __launch_bounds__(kTileThreads) tile_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(const AppendParams p) {
   using SM = TileSmem<D, R>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   SM& S = *reinterpret_cast<SM*>(smem_raw);
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.y;
-  const int t0 = blockIdx.x * kTileTokens;
-  const int nt = min(kTileTokens, p.n_new - t0);
-  if (tid < kTileTokens) S.row[tid] = tid < nt ? token_row(p, t0 + tid, h) : -1;
+  const int tiles = (p.n_new + kTileTokens - 1) / kTileTokens;
+  constexpr int PPR = D / 8, PER = kTileTokens * PPR / kTileThreads;
+  // A tile's keys are asked for, and its cache rows looked up, while the tile before is worked on.
+  auto ask = [&](int tile, int buf) {
+    const int t0 = tile * kTileTokens, nt = min(kTileTokens, p.n_new - t0);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = tid + i * kTileThreads, t = e / PPR, c = e % PPR;
+      if (t < nt) copy_async16(&S.K[buf][t][c * 16], p.K_new + (size_t)(t0 + t) * p.kv_stride + (size_t)h * D + c * 8);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (tid < kTileTokens) S.row[buf][tid] = tid < nt ? token_row(p, t0 + tid, h) : -1;
+  };
+  ask(blockIdx.x, 0);
   if (p.Kproj != nullptr) {
     // M[h] is [R][D]: a thread moves 4 channels of one output (outputs vary fastest over the
     // lanes, so that the transposed stores of a warp fall into different banks)
+#pragma unroll 4
     for (int e = tid; e < R * D / 4; e += kTileThreads) {
       const int j = e % R, c = (e / R) * 4;
-      const float4 m = *reinterpret_cast<const float4*>(p.M + ((size_t)h * R + j) * D + c);
+      const float4 m = __ldg(reinterpret_cast<const float4*>(p.M + ((size_t)h * R + j) * D + c));
       S.Mt[c][j] = m.x;
       S.Mt[c + 1][j] = m.y;
       S.Mt[c + 2][j] = m.z;
       S.Mt[c + 3][j] = m.w;
     }
   }
-  constexpr int PPR = D / 8;
-  for (int e = tid; e < nt * PPR; e += kTileThreads) {
-    const int t = e / PPR, c = e % PPR;
-    *reinterpret_cast<uint4*>(&S.K[t][c * 16]) =
-        ldg_stream128(p.K_new + (size_t)(t0 + t) * p.kv_stride + (size_t)h * D + c * 8);
-  }
-  __syncthreads();
-  for (int e = tid; e < nt * PPR; e += kTileThreads) {
-    const int t = e / PPR, c = e % PPR;
-    const uint4 v = ldg_stream128(p.V_new + (size_t)(t0 + t) * p.kv_stride + (size_t)h * D + c * 8);
-    const long long row = S.row[t];
-    if (row >= 0) {
-      *reinterpret_cast<uint4*>(p.K + (size_t)row * D + c * 8) = *reinterpret_cast<const uint4*>(&S.K[t][c * 16]);
-      *reinterpret_cast<uint4*>(p.V + (size_t)row * D + c * 8) = v;
+  int buf = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    const int t0 = tile * kTileTokens, nt = min(kTileTokens, p.n_new - t0);
+    uint4 vr[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = tid + i * kTileThreads, t = e / PPR, c = e % PPR;
+      if (t < nt) vr[i] = ldg_stream128(p.V_new + (size_t)(t0 + t) * p.kv_stride + (size_t)h * D + c * 8);
     }
-  }
-  if (p.Kproj == nullptr) return;
-
-  // Unit u: outputs 8 * (u / 32) .. + 7 of tokens u % 32 and u % 32 + 32.
-  constexpr int BLK = D / 8;
-  for (int u = tid; u < (kTileTokens / 2) * (R / 8); u += kTileThreads) {
-    const int ta = u % 32, tb = ta + 32, j0 = (u / 32) * 8;
-    if (ta >= nt) continue;
-    float2 tot[2][4];  // p0+p1, then the running combination
-    float2 hold[2][4], hold2[2][4];
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    if (tile + (int)gridDim.x < tiles) ask(tile + gridDim.x, buf ^ 1);
 #pragma unroll
-    for (int blk = 0; blk < 8; ++blk) {
-      float2 a[2][4];
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[x][i] = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int c2 = 0; c2 < BLK / 2; ++c2) {
-        const int c = blk * BLK + c2 * 2;
-        const uint32_t ka = *reinterpret_cast<const uint32_t*>(&S.K[ta][c * 2]);
-        const uint32_t kb = *reinterpret_cast<const uint32_t*>(&S.K[tb][c * 2]);
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const float4 m0 = *reinterpret_cast<const float4*>(&S.Mt[c + o][j0]);
-          const float4 m1 = *reinterpret_cast<const float4*>(&S.Mt[c + o][j0 + 4]);
-          const float fa = o ? bf16hi(ka) : bf16lo(ka), fb = o ? bf16hi(kb) : bf16lo(kb);
-          const float2 xa = make_float2(fa, fa), xb = make_float2(fb, fb);
-          const float2 mm[4] = {make_float2(m0.x, m0.y), make_float2(m0.z, m0.w), make_float2(m1.x, m1.y),
-                                make_float2(m1.z, m1.w)};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a[0][i] = ffma2(mm[i], xa, a[0][i]);
-            a[1][i] = ffma2(mm[i], xb, a[1][i]);
-          }
-        }
+    for (int i = 0; i < PER; ++i) {
+      const int e = tid + i * kTileThreads, t = e / PPR, c = e % PPR;
+      const long long to = S.row[buf][t];
+      if (to >= 0) {
+        *reinterpret_cast<uint4*>(p.K + (size_t)to * D + c * 8) = *reinterpret_cast<const uint4*>(&S.K[buf][t][c * 16]);
+        *reinterpret_cast<uint4*>(p.V + (size_t)to * D + c * 8) = vr[i];
       }
-      // ((p0+p1)+(p2+p3)) + ((p4+p5)+(p6+p7)), as the partial sums arrive
+    }
+    if (p.Kproj != nullptr) {
+      // A lane takes tokens lane, lane + 32, + 64, + 96, a warp OUT outputs at a time: one load of M
+      // (the same for the warp) feeds 4 tokens, one 16-byte load of a row 8 channels.
+      constexpr int BLK = D / 8, OUT = R == 16 ? 2 : 4, P2 = OUT / 2, TK = 4;
+#pragma unroll 1
+      for (int j0 = warp * OUT; j0 < R; j0 += kTileThreads / 32 * OUT) {
+        asm volatile("" ::: "memory");  // the keys are read again for the next outputs, not kept
+        float2 tot[TK][P2], hold[TK][P2], hold2[TK][P2];  // the running combination of the 8 partial sums
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+        for (int blk = 0; blk < 8; ++blk) {
+          float2 a[TK][P2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = a[x][i];
-          if (blk % 2 == 0) {
-            hold[x][i] = v;
-          } else {
-            const float2 pr = make_float2(hold[x][i].x + v.x, hold[x][i].y + v.y);
-            if (blk % 4 == 1) {
-              hold2[x][i] = pr;
-            } else {
-              const float2 q = make_float2(hold2[x][i].x + pr.x, hold2[x][i].y + pr.y);
-              if (blk == 3) tot[x][i] = q;
-              else tot[x][i] = make_float2(tot[x][i].x + q.x, tot[x][i].y + q.y);
+          for (int x = 0; x < TK; ++x)
+#pragma unroll
+            for (int i = 0; i < P2; ++i) a[x][i] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c8 = 0; c8 < BLK / 8; ++c8) {
+            const int c0 = blk * BLK + c8 * 8;
+            uint32_t k[TK][4];
+#pragma unroll
+            for (int x = 0; x < TK; ++x)
+              *reinterpret_cast<uint4*>(k[x]) = *reinterpret_cast<const uint4*>(&S.K[buf][lane + 32 * x][c0 * 2]);
+#pragma unroll
+            for (int o = 0; o < 8; ++o) {
+              float2 mm[P2];
+              if constexpr (OUT == 4) *reinterpret_cast<float4*>(mm) = *reinterpret_cast<const float4*>(&S.Mt[c0 + o][j0]);
+              else mm[0] = *reinterpret_cast<const float2*>(&S.Mt[c0 + o][j0]);
+#pragma unroll
+              for (int x = 0; x < TK; ++x) {
+                const float f = o & 1 ? bf16hi(k[x][o / 2]) : bf16lo(k[x][o / 2]);
+#pragma unroll
+                for (int i = 0; i < P2; ++i) a[x][i] = ffma2(mm[i], make_float2(f, f), a[x][i]);
+              }
             }
           }
+          // ((p0+p1)+(p2+p3)) + ((p4+p5)+(p6+p7)), as the partial sums arrive
+#pragma unroll
+          for (int x = 0; x < TK; ++x)
+#pragma unroll
+            for (int i = 0; i < P2; ++i) {
+              const float2 v = a[x][i];
+              if (blk % 2 == 0) {
+                hold[x][i] = v;
+              } else {
+                const float2 pr = make_float2(hold[x][i].x + v.x, hold[x][i].y + v.y);
+                if (blk % 4 == 1) {
+                  hold2[x][i] = pr;
+                } else {
+                  const float2 q = make_float2(hold2[x][i].x + pr.x, hold2[x][i].y + pr.y);
+                  if (blk == 3) tot[x][i] = q;
+                  else tot[x][i] = make_float2(tot[x][i].x + q.x, tot[x][i].y + q.y);
+                }
+              }
+            }
         }
-    }
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int t = x ? tb : ta;
-      const long long row = t < nt ? S.row[t] : -1;
-      if (row < 0) continue;
-      if constexpr (FP8) {
-        const float s = p.kproj_scale[h];
-        uint32_t w[2];
+        for (int x = 0; x < TK; ++x) {
+          const long long row = S.row[buf][lane + 32 * x];
+          if (row < 0) continue;
+          const size_t at = (size_t)row * R + j0;
+          if constexpr (FP8) {
+            const float s = p.kproj_scale[h];
+            unsigned char* dst = static_cast<unsigned char*>(p.Kproj) + at;
+            const uint32_t lo = (uint32_t)fp8_of(tot[x][0].x, s) | ((uint32_t)fp8_of(tot[x][0].y, s) << 8);
+            if constexpr (OUT == 4)
+              *reinterpret_cast<uint32_t*>(dst) =
+                  lo | ((uint32_t)fp8_of(tot[x][P2 - 1].x, s) << 16) | ((uint32_t)fp8_of(tot[x][P2 - 1].y, s) << 24);
+            else *reinterpret_cast<unsigned short*>(dst) = (unsigned short)lo;
+          } else {
+            __align__(8) __nv_bfloat162 w[P2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          w[i] = (uint32_t)fp8_of(tot[x][2 * i].x, s) | ((uint32_t)fp8_of(tot[x][2 * i].y, s) << 8) |
-                 ((uint32_t)fp8_of(tot[x][2 * i + 1].x, s) << 16) | ((uint32_t)fp8_of(tot[x][2 * i + 1].y, s) << 24);
-        *reinterpret_cast<uint2*>(static_cast<unsigned char*>(p.Kproj) + (size_t)row * R + j0) = make_uint2(w[0], w[1]);
-      } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 pr = __floats2bfloat162_rn(tot[x][i].x, tot[x][i].y);
-          w[i] = *reinterpret_cast<const uint32_t*>(&pr);
+            for (int i = 0; i < P2; ++i) w[i] = __floats2bfloat162_rn(tot[x][i].x, tot[x][i].y);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.Kproj) + at;
+            if constexpr (OUT == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(w);
+            else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(w);
+          }
         }
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.Kproj) + (size_t)row * R + j0) =
-            make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
+    __syncthreads();  // this buffer's keys and rows have been used before they are asked for again
   }
 }
 
@@ -260,8 +286,11 @@ cudaError_t launch_drf(const AppendParams& p, int sms, cudaStream_t stream) {
   const int smem = (int)sizeof(TileSmem<D, R>);
   const cudaError_t e = prepare_kernel((const void*)kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)((p.n_new + kTileTokens - 1) / kTileTokens), (unsigned)p.Hkv),
-                    dim3(kTileThreads), (size_t)smem, stream, p);
+  // As many CTAs as are resident at once share the tiles of all heads.
+  const int tiles = (p.n_new + kTileTokens - 1) / kTileTokens;
+  const int per_head = (sms * ctas_per_sm((const void*)kern, kTileThreads, smem) + p.Hkv - 1) / p.Hkv;
+  return launch_pdl(kern, dim3((unsigned)(tiles < per_head ? tiles : per_head), (unsigned)p.Hkv), dim3(kTileThreads), (size_t)smem,
+                    stream, p);
 }
 
 template <int D>
