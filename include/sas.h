@@ -243,7 +243,10 @@ sas_status sas_gather_selected(const sas_shape* shape, const void* K, const void
  * hold anything, NaN and infinities among it.
  *
  * Each of these calls shares a workspace with the calls above under the same rule (one shape,
- * stream-ordered, sas_workspace_init once). */
+ * stream-ordered, sas_workspace_init once, and again after a reported device error 5, a wait that
+ * ran out).  sas_chunk_workspace_bytes never falls as n_new grows: a workspace for many new tokens
+ * serves calls with few.  The contiguous or paged cache holds fewer than 2^31 - 64 rows in
+ * sas_chunk_attention and sas_window_decode.  n_new is 1 to 2^22. */
 
 /* Rows of a chunk into the caches: K, V and, unless Kproj is NULL, the projected rows.
  *   K_new, V_new bf16 [n_new][Hkv][d], kv_stride elements apart per token (>= Hkv * d)

@@ -958,8 +958,10 @@ cudaError_t launch_d(const ChunkParams& p, cudaStream_t stream) {
   return launch_pdl(join_kernel<D>, dim3((unsigned)((p.ctas - 1) * p.waves_max)), dim3(kJoinThreads), 0, stream, p);
 }
 
+// Never less for more new tokens, so that a workspace for many serves a call with few.
 size_t task_bytes(const ChunkParams& p) {
-  return ((size_t)(p.own_plan ? kChunkMaxCtas : 1) * (p.slots + 1) * sizeof(ChunkTask) + 255) & ~(size_t)255;
+  const size_t own = (size_t)kChunkMaxCtas * ((p.slots < kOwnPlanSlots ? p.slots : kOwnPlanSlots) + 1), one = (size_t)p.slots + 1;
+  return ((own > one ? own : one) * sizeof(ChunkTask) + 255) & ~(size_t)255;
 }
 
 }  // namespace

@@ -5,6 +5,8 @@ all the work.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
+
 import torch
 
 from . import lib
@@ -48,6 +50,7 @@ class DecodeSession:
         self.ws_bytes = nbytes
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         lib.sas_workspace_init(self.workspace, nbytes)
+        self.device = self.workspace.device
         self.out = torch.empty(shape.B, shape.Hq, shape.d, dtype=torch.float32, device=device)
         self.idx = torch.empty(shape.B, shape.Hkv, self.k_max, dtype=torch.int32, device=device)
 
@@ -75,13 +78,22 @@ class DecodeSession:
                                  out, self.workspace, self.ws_bytes)
         return out
 
+    def _on_device(self, *tensors):
+        """The session's device as the current one, for tensors that all lie there."""
+        index = self.device.index
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                raise ValueError(f"a tensor lies on {t.device}, the session on {self.device}")
+        return nullcontext() if torch.cuda.current_device() == index else torch.cuda.device(index)
+
     def append_chunk(self, K_new, V_new, q_start, M, K, V, Kproj, page_table, seqlens):
         """K_new, V_new [n_new][Hkv][d], tokens at any stride; Kproj (and M) may be None."""
         n_new, stride = _tokens(K_new, self.shape.Hkv, self.shape.d, "K_new")
         if _tokens(V_new, self.shape.Hkv, self.shape.d, "V_new") != (n_new, stride):
             raise ValueError("K_new and V_new differ in tokens or stride")
-        lib.sas_append_chunk(self.shape, K_new, V_new, stride, q_start, n_new, M, K, V, Kproj, page_table, seqlens,
-                             self.workspace, self.ws_bytes)
+        with self._on_device(K_new, V_new, q_start, M, K, V, Kproj, page_table, seqlens):
+            lib.sas_append_chunk(self.shape, K_new, V_new, stride, q_start, n_new, M, K, V, Kproj, page_table, seqlens,
+                                 self.workspace, self.ws_bytes)
 
     def chunk(self, q, q_start, K, V, page_table, seqlens, window=0, sinks=0, out=None, lse=None):
         """q [n_new][Hq][d], tokens at any stride.  Returns out (bf16) and lse (None unless given)."""
@@ -90,23 +102,28 @@ class DecodeSession:
             raise ValueError(f"{n_new} new tokens, more than the session's {self.chunk_max}")
         if out is None:
             out = torch.empty(n_new, self.shape.Hq, self.shape.d, dtype=torch.bfloat16, device=q.device)
-        lib.sas_chunk_attention(self.shape, q, stride, q_start, n_new, K, V, page_table, seqlens, window, sinks, out,
-                                lse, self.workspace, self.ws_bytes)
+        with self._on_device(q, q_start, K, V, page_table, seqlens, out, lse):
+            lib.sas_chunk_attention(self.shape, q, stride, q_start, n_new, K, V, page_table, seqlens, window, sinks, out,
+                                    lse, self.workspace, self.ws_bytes)
         return out, lse
 
     def window(self, q, K, V, page_table, seqlens, window, sinks=0, weights=None, out=None, lse=None):
+        """The newest token of every sequence.  Adds the softmax weights to `weights` unless None."""
         out = self.out if out is None else out
-        lib.sas_window_decode(self.shape, q, K, V, page_table, seqlens, window, sinks, out, lse, weights,
-                              self.workspace, self.ws_bytes)
+        with self._on_device(q, K, V, page_table, seqlens, weights, out, lse):
+            lib.sas_window_decode(self.shape, q, K, V, page_table, seqlens, window, sinks, out, lse, weights,
+                                  self.workspace, self.ws_bytes)
         return out, lse
 
     def evict(self, weights, keep, sinks, recent, K, V, Kproj, log_g, page_table, seqlens, idx=None, weights_out=None,
               seqlens_out=None):
         """In place by default: weights and seqlens are updated where they are."""
         idx = self.idx if idx is None else idx
-        lib.sas_evict(self.shape, weights, keep, self.k_max, sinks, recent, K, V, Kproj, log_g, page_table, seqlens,
-                      idx, weights if weights_out is None else weights_out,
-                      seqlens if seqlens_out is None else seqlens_out, self.workspace, self.ws_bytes)
+        weights_out = weights if weights_out is None else weights_out
+        seqlens_out = seqlens if seqlens_out is None else seqlens_out
+        with self._on_device(weights, keep, K, V, Kproj, log_g, page_table, seqlens, idx, weights_out, seqlens_out):
+            lib.sas_evict(self.shape, weights, keep, self.k_max, sinks, recent, K, V, Kproj, log_g, page_table, seqlens,
+                          idx, weights_out, seqlens_out, self.workspace, self.ws_bytes)
         return idx
 
     def check(self):
