@@ -41,7 +41,8 @@ struct Geo {
   static constexpr int HALF_BYTES = kTile * 128;           // 128 rows of 64 columns
   static constexpr int TILE_BYTES = HALVES * HALF_BYTES;   // Q tile, K block or V block
   static constexpr int STAGES = D == 128 ? 5 : 8;
-  static constexpr int SMEM = 1024 + (2 + STAGES) * TILE_BYTES;
+  static constexpr int Q_BUFS = D == 128 ? 1 : 2;          // tasks whose Q is held: the next one's comes ahead
+  static constexpr int SMEM = 1024 + (2 * Q_BUFS + STAGES) * TILE_BYTES;
   // Tensor memory, 512 columns: P of the tiles (64 each), S, O of the tiles.  At d = 128 the tiles
   // share one S; at d = 64 there is room for two.
   static constexpr int S_BUFS = D == 128 ? 1 : 2;
@@ -377,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   constexpr int ST = Gm::STAGES;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  unsigned char* ring = qs + 2 * Gm::TILE_BYTES;
-  __shared__ uint64_t full[ST], empty[ST], q_full, q_empty, s_full[2], s_read[2], p_ready[2], pv_done[2], half_full, half_free, drain;
+  unsigned char* ring = qs + 2 * Gm::Q_BUFS * Gm::TILE_BYTES;
+  __shared__ uint64_t full[ST], empty[ST], q_full[Gm::Q_BUFS], q_empty[Gm::Q_BUFS], s_full[2], s_read[2], p_ready[2], pv_done[2], half_full, half_free, drain;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int stop_s;
   __shared__ const ChunkTask* volatile list_s;
@@ -390,8 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(&q_full, 1);
-    mbar_init(&q_empty, 1);
+    for (int i = 0; i < Gm::Q_BUFS; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_ready[t], 4);
@@ -450,19 +453,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int be = (int)min((long long)t.blocks, c.block + (u1 - u)), units_here = be - c.block;
       const bool one = t.ntok <= p.tok_tile;
       const VisiblePages vis = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks);
-      if (lane == 0) {
-        live = seg == 0 || wait_live(&q_empty, (seg - 1) & 1, &stop_s);
-        if (live) {
-          const int box = p.G * p.tok_tile * 128;
-          mbar_arrive_expect_tx(&q_full, (one ? 1 : 2) * Gm::HALVES * box);
-          for (int i = 0; i < (one ? 1 : 2); ++i)
-#pragma unroll
-            for (int hf = 0; hf < Gm::HALVES; ++hf)
-              tma_3d(qs + i * Gm::TILE_BYTES + hf * Gm::HALF_BYTES, &p.qmap, hf * 64, c.h * p.G, t.tok0 + i * p.tok_tile, &q_full);
-        }
-      }
-      live = __shfl_sync(0xffffffffu, live, 0);
-      if (live) ++seg;
       // rows of 32 pages, page v with lane v % 32, looked up 16 at a time
       int row = 0, have = c.block * (one ? 4 : 2);
       auto push = [&](const CUtensorMap* map, int v) {
@@ -500,9 +490,28 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         live = __shfl_sync(0xffffffffu, live, 0);
         if (live) ++cnt;
       };
+      auto load_q = [&] {
+        const int qb = seg % Gm::Q_BUFS;
+        if (lane == 0 && live) {
+          live = seg < Gm::Q_BUFS || wait_live(&q_empty[qb], ((seg / Gm::Q_BUFS) & 1) ^ 1, &stop_s);
+          if (live) {
+            const int box = p.G * p.tok_tile * 128;
+            mbar_arrive_expect_tx(&q_full[qb], (one ? 1 : 2) * Gm::HALVES * box);
+            for (int i = 0; i < (one ? 1 : 2); ++i)
+#pragma unroll
+              for (int hf = 0; hf < Gm::HALVES; ++hf)
+                tma_3d(qs + (2 * qb + i) * Gm::TILE_BYTES + hf * Gm::HALF_BYTES, &p.qmap, hf * 64, c.h * p.G,
+                       t.tok0 + i * p.tok_tile, &q_full[qb]);
+          }
+        }
+        live = __shfl_sync(0xffffffffu, live, 0);
+        if (live) ++seg;
+      };
+      // the first keys do not wait for the room that Q waits for
       if (one) {
         push(&p.kmap, 4 * c.block);
         push(&p.kmap, 4 * c.block + 2);
+        load_q();
         for (int j = c.block; j < be; ++j)
           for (int x = 0; x < 2; ++x) {
             if (j + 1 < be) push(&p.kmap, 4 * j + 4 + 2 * x);
@@ -510,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           }
       } else {
         push(&p.kmap, 2 * c.block);
+        load_q();
         for (int j = c.block; j < be; ++j) {
           if (j + 1 < be) push(&p.kmap, 2 * j + 2);
           push(&p.vmap, 2 * j);
@@ -521,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
     // after a wait that ran out: the copies in flight land before the CTA ends
     if (lane == 0 && !live) {
-      if (seg > 0) mbar_wait_bounded(&q_full, (seg - 1) & 1);
+      for (int i = max(0, seg - Gm::Q_BUFS); i < seg; ++i) mbar_wait_bounded(&q_full[i % Gm::Q_BUFS], (i / Gm::Q_BUFS) & 1);
       for (int i = max(0, cnt - ST); i < cnt; ++i) mbar_wait_bounded(&full[i % ST], (i / ST) & 1);
     }
   } else if (warp == 8) {
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       bool live = true;
       auto scores = [&](int x, bool one) {  // S = Q K^T for warpgroup x, K in ring place k
         const int buf = Gm::S_BUFS == 1 ? 0 : x;
-        const uint64_t a = qd + (one ? 0 : x) * kStep, b = kd + k.st * kStep;
+        const uint64_t a = qd + (2 * (seg % Gm::Q_BUFS) + (one ? 0 : x)) * kStep, b = kd + k.st * kStep;
         live = live && wait_warp(&full[k.st], k.ph, &stop_s);
         live = live && wait_warp(&s_read[buf], ph_read, &stop_s);  // the scores that were there have been read
         if (Gm::S_BUFS == 1 || x == 1) ph_read ^= 1;
@@ -561,13 +571,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const ChunkTask t = list[c.task];
         const int n = (int)min((long long)t.blocks - c.block, u1 - u);
         const bool one = t.ntok <= p.tok_tile;
-        live = wait_warp(&q_full, seg & 1, &stop_s);
+        live = wait_warp(&q_full[seg % Gm::Q_BUFS], (seg / Gm::Q_BUFS) & 1, &stop_s);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (x == 0 || one) k = r.take<ST>();
           scores(x, one);
         }
-        if (n == 1 && live) tc_commit(&q_empty, lead);
+        if (n == 1 && live) tc_commit(&q_empty[seg % Gm::Q_BUFS], lead);
         for (int j = 0; j < n && live; ++j) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -575,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (j + 1 < n) {
               if (x == 0 || one) k = r.take<ST>();
               scores(x, one);
-              if (j + 2 == n && x == 1 && live) tc_commit(&q_empty, lead);
+              if (j + 2 == n && x == 1 && live) tc_commit(&q_empty[seg % Gm::Q_BUFS], lead);
             }
             if (x == 0 || one) v = r.take<ST>();
             const uint64_t b = vd + v.st * kStep;
@@ -673,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             ph_s ^= 1;
             tc_fence_after();
             if (j < plain0 || j >= plain1) {
-              // Scores that a row does not see are overwritten where they lie, 8 at a time.
+              // Scores that a row does not see are overwritten where they lie.
               clear_row(j);
               const GroupSeg g(p, list_s, c, x);
               const int pos = g.plo + r / p.G, wlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
@@ -685,14 +695,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                   see = v < g.vis.nv ? low_bits(pos + 1 - j0) & (~low_bits(wlo - j0) | low_bits(p.sinks - j0)) : 0;
                 if (__all_sync(0xffffffffu, see == ~0ull)) continue;
 #pragma unroll 1
-                for (int k = 0; k < kPage; k += 8, see >>= 8) {
-                  float y[8];
-                  tmem_ld8(y, tS + i * kPage + k);
+                for (int k = 0; k < kPage; k += 32, see >>= 32) {
+                  float y[32];
+                  tmem_ld32(y, tS + i * kPage + k);
                   tmem_wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 8; ++e)
+                  for (int e = 0; e < 32; ++e)
                     if (!((uint32_t)see & (1u << e))) y[e] = -INFINITY;
-                  tmem_st8(tS + i * kPage + k, y);
+                  tmem_st16(tS + i * kPage + k, reinterpret_cast<const uint32_t*>(y));
+                  tmem_st16(tS + i * kPage + k + 16, reinterpret_cast<const uint32_t*>(y) + 16);
                 }
               }
               tmem_wait_st();
