@@ -260,6 +260,24 @@ def test_chunk_large(cuda_lib, B, Hq, Hkv, d, lens, new, paged, window):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,d,n,T,paged", [
+    (32, 8, 128, 20000, 600, True),     # two waves of KV heads, lists made by the CTAs
+    (16, 8, 64, 45000, 1500, False),
+    (32, 8, 128, 19500, 19500, True),   # and a list made beforehand
+    (24, 6, 128, 90000, 500, False),    # four waves of one or two heads
+])
+def test_chunk_waves(cuda_lib, Hq, Hkv, d, n, T, paged):
+    p = make_problem(B=1, Hq=Hq, Hkv=Hkv, d=d, r=16, seqlens=[n], k=1, paged=paged, seed=7)
+    c = p.to("cuda")
+    s = lib_and_session(c, chunk=T)
+    q = torch.randn(T, Hq, d, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16)
+    lse = torch.empty(T, Hq, device="cuda")
+    out, _ = s.chunk(q.cuda(), starts_of([T]).cuda(), c.K, c.V, c.page_table, c.seqlens, lse=lse)
+    assert s.check()[0] == 0
+    check_rows(p, q, out, lse, [T], 0, 0, [(0, t) for t in (0, 33, 64, T // 2, T - 65, T - 1)])
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits(cuda_lib):
     """A cache of 2.4e9 elements per array: the last head lies behind every 32-bit element offset."""
     H, n, d, T, W = 72, 262144, 128, 40, 300

@@ -12,13 +12,29 @@
 //              (drafted tokens and short chunks: the cache is read at twice the rate per step).
 // A share that holds part of a task leaves a partial (m, l, O); join_kernel puts those together in order.
 //
-// CTA: two softmax warpgroups (a thread is a row), one thread that issues the matrix
-// instructions, one warp that loads.  S = Q K^T goes to tensor memory; the softmax threads read
-// their row, write P in bf16 over it, and P V takes its left operand from there, so P never
-// passes through shared memory.  The two tiles alternate: while one is exponentiated, the
-// other's products run.  O is rescaled only when a row's maximum has grown by 2^8 since the last
-// time (P <= 2^8 keeps bf16's relative rounding and fp32's range), which after the first blocks is rare.
+// The KV heads are gone through in waves whose K and V stay in L2 (struct Wave).
+//
+// CTA: two softmax warpgroups (a thread is a row), one warp that issues the matrix instructions,
+// one warp that loads.  S = Q K^T goes to tensor memory; the softmax threads read their row and
+// write P in bf16 back to tensor memory, where P V takes its left operand from, so P never passes
+// through shared memory.  Tensor memory (512 columns) holds P and O of both tiles and, with
+// d = 128, one S that the tiles use in turn: it is free again as soon as its rows have been read,
+// and the next tile's S is made while this one is exponentiated.  O is rescaled only when a row's
+// maximum has grown by 2^8 since the last time (P <= 2^8 keeps bf16's relative rounding and fp32's
+// range), which after the first blocks is rare.  Sums and maxima are fp32; P is rounded to bf16,
+// which the matrix instructions take, and that rounding (2^-8 of a weight) bounds the error.
 // K and V blocks of 128 keys pass through one ring of tiled bulk copies (128-byte swizzle).
+//
+// What bounds it, for two-tile units with d = 128: a unit is 2048 cycles of matrix instructions and
+// takes about 2900.  Shared memory gives 128 bytes a cycle and Q K^T alone takes that, so every
+// byte the copies write (64 KB a unit) and V's reads stretch it; with the softmax left out a unit
+// still took 2800.  Measured: prompt of 8192 (32 heads, 8 KV heads) 561 us, 980 TFLOP/s; 512 tokens
+// on 32K rows 265 us, 1030 TFLOP/s, both at the 1.1-1.3 GHz that the power limit leaves; 8 x 5
+// tokens on 4K to 32K rows 116 us, 5.2 TB/s.  With d = 64 the loop over blocks (3100 cycles) and the
+// ends of tasks (4000 each) bound it.
+// Tried and not kept: a warp for each of the two products (384K cycles against 345K for 512 on
+// 32K); polynomial exponentials on the FMA pipe for part of the row (286 us without, 288 to 316 us
+// with); P in the place of S (a tile's products then wait for its softmax).
 #include "sas_device.cuh"
 #include "sas_kernels.h"
 
@@ -31,8 +47,10 @@ constexpr int kPlanThreads = 1024;
 constexpr int kOwnPlanSlots = 256;   // up to so many task slots every CTA makes the list itself
 constexpr int kTile = 128;
 constexpr int kRowsCap = 2 * kTile;  // rows of a partial
-constexpr long long kLiveBytes = 48LL << 20;
-constexpr int kWaveUnits = 24;
+// K and V bytes of a wave: more do not stay in the 126 MB of L2, fewer waves leave fewer partials
+// (512 tokens on 32K rows, 128 MB: one wave 284 us, two 264 us, three 280 us).
+constexpr long long kLiveBytes = 72LL << 20;
+constexpr int kWaveUnits = 24;       // units of a CTA and wave that a partial per wave is worth
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D>
