@@ -5,8 +5,6 @@ all the work.
 """
 from __future__ import annotations
 
-from contextlib import nullcontext
-
 import torch
 
 from . import lib
@@ -14,12 +12,12 @@ from . import lib
 
 def _tokens(x, heads: int, d: int, name: str):
     """Tokens and token stride of a bf16 [n][heads][d] tensor whose heads are dense."""
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d:
-        raise ValueError(f"{name} must be bf16 [tokens][{heads}][{d}], got {x.dtype} {tuple(x.shape)}")
-    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+    size, step = tuple(x.shape), x.stride()
+    if x.dtype != torch.bfloat16 or size[1:] != (heads, d) or len(size) != 3:
+        raise ValueError(f"{name} must be bf16 [tokens][{heads}][{d}], got {x.dtype} {size}")
+    if step[2] != 1 or (heads > 1 and step[1] != d):
         raise ValueError(f"{name}: the heads of a token must lie one after another")
-    n = x.shape[0]
-    return n, x.stride(0) if n > 1 else max(x.stride(0), heads * d)
+    return size[0], step[0] if size[0] > 1 else heads * d
 
 
 class DecodeSession:
@@ -78,22 +76,25 @@ class DecodeSession:
                                  out, self.workspace, self.ws_bytes)
         return out
 
-    def _on_device(self, *tensors):
-        """The session's device as the current one, for tensors that all lie there."""
+    def _run(self, call, tensors, *args):
+        """A call on the session's device and that device's current stream; every tensor lies there."""
         index = self.device.index
         for t in tensors:
             if t is not None and t.get_device() != index:
                 raise ValueError(f"a tensor lies on {t.device}, the session on {self.device}")
-        return nullcontext() if torch.cuda.current_device() == index else torch.cuda.device(index)
+        if torch.cuda.current_device() == index:
+            call(self.shape, *args, self.workspace, self.ws_bytes, lib._raw_stream(index))
+        else:
+            with torch.cuda.device(index):
+                call(self.shape, *args, self.workspace, self.ws_bytes, lib._raw_stream(index))
 
     def append_chunk(self, K_new, V_new, q_start, M, K, V, Kproj, page_table, seqlens):
         """K_new, V_new [n_new][Hkv][d], tokens at any stride; Kproj (and M) may be None."""
         n_new, stride = _tokens(K_new, self.shape.Hkv, self.shape.d, "K_new")
         if _tokens(V_new, self.shape.Hkv, self.shape.d, "V_new") != (n_new, stride):
             raise ValueError("K_new and V_new differ in tokens or stride")
-        with self._on_device(K_new, V_new, q_start, M, K, V, Kproj, page_table, seqlens):
-            lib.sas_append_chunk(self.shape, K_new, V_new, stride, q_start, n_new, M, K, V, Kproj, page_table, seqlens,
-                                 self.workspace, self.ws_bytes)
+        self._run(lib.sas_append_chunk, (K_new, V_new, q_start, M, K, V, Kproj, page_table, seqlens), K_new, V_new, stride,
+                  q_start, n_new, M, K, V, Kproj, page_table, seqlens)
 
     def chunk(self, q, q_start, K, V, page_table, seqlens, window=0, sinks=0, out=None, lse=None):
         """q [n_new][Hq][d], tokens at any stride.  Returns out (bf16) and lse (None unless given)."""
@@ -102,17 +103,15 @@ class DecodeSession:
             raise ValueError(f"{n_new} new tokens, more than the session's {self.chunk_max}")
         if out is None:
             out = torch.empty(n_new, self.shape.Hq, self.shape.d, dtype=torch.bfloat16, device=q.device)
-        with self._on_device(q, q_start, K, V, page_table, seqlens, out, lse):
-            lib.sas_chunk_attention(self.shape, q, stride, q_start, n_new, K, V, page_table, seqlens, window, sinks, out,
-                                    lse, self.workspace, self.ws_bytes)
+        self._run(lib.sas_chunk_attention, (q, q_start, K, V, page_table, seqlens, out, lse), q, stride, q_start, n_new, K, V,
+                  page_table, seqlens, window, sinks, out, lse)
         return out, lse
 
     def window(self, q, K, V, page_table, seqlens, window, sinks=0, weights=None, out=None, lse=None):
         """The newest token of every sequence.  Adds the softmax weights to `weights` unless None."""
         out = self.out if out is None else out
-        with self._on_device(q, K, V, page_table, seqlens, weights, out, lse):
-            lib.sas_window_decode(self.shape, q, K, V, page_table, seqlens, window, sinks, out, lse, weights,
-                                  self.workspace, self.ws_bytes)
+        self._run(lib.sas_window_decode, (q, K, V, page_table, seqlens, weights, out, lse), q, K, V, page_table, seqlens,
+                  window, sinks, out, lse, weights)
         return out, lse
 
     def evict(self, weights, keep, sinks, recent, K, V, Kproj, log_g, page_table, seqlens, idx=None, weights_out=None,
@@ -121,9 +120,9 @@ class DecodeSession:
         idx = self.idx if idx is None else idx
         weights_out = weights if weights_out is None else weights_out
         seqlens_out = seqlens if seqlens_out is None else seqlens_out
-        with self._on_device(weights, keep, K, V, Kproj, log_g, page_table, seqlens, idx, weights_out, seqlens_out):
-            lib.sas_evict(self.shape, weights, keep, self.k_max, sinks, recent, K, V, Kproj, log_g, page_table, seqlens,
-                          idx, weights_out, seqlens_out, self.workspace, self.ws_bytes)
+        self._run(lib.sas_evict, (weights, keep, K, V, Kproj, log_g, page_table, seqlens, idx, weights_out, seqlens_out),
+                  weights, keep, self.k_max, sinks, recent, K, V, Kproj, log_g, page_table, seqlens, idx, weights_out,
+                  seqlens_out)
         return idx
 
     def check(self):
