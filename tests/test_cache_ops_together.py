@@ -185,6 +185,20 @@ def test_bad_chunks_are_reported_and_skipped(cuda_lib):
 
 
 @pytest.mark.gpu
+def test_nothing_new(cuda_lib):
+    """Rows that belong to no sequence, and no row that does: nothing is written, nothing reported."""
+    p = make_problem(B=2, Hq=4, Hkv=2, d=64, r=16, seqlens=[0, 70], k=1, paged=True, seed=4).to("cuda")
+    s = lib_and_session(p, chunk=3)
+    q = torch.randn(3, 4, 64, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    K, V = p.K.clone(), p.V.clone()
+    start = starts_of([0, 0]).cuda()
+    s.append_chunk(q[:, :2], q[:, 2:], start, None, K, V, None, p.page_table, p.seqlens)
+    s.chunk(q, start, K, V, p.page_table, p.seqlens, out=out)
+    assert s.check()[0] == 0 and (out == 7).all() and torch.equal(K, p.K) and torch.equal(V, p.V)
+
+
+@pytest.mark.gpu
 def test_evict_bad_values_are_reported(cuda_lib):
     p = make_problem(B=2, Hq=2, Hkv=2, d=64, r=16, seqlens=[300, 200], k=1, paged=True, seed=4).to("cuda")
     s = lib_and_session(p, k_max=50, evict=True)

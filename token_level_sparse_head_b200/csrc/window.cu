@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------------ producer
-    int cnt = 0;
+    int cnt = 0, sent = 0;
     for (int u = u0; u < u1;) {
       const int n = seq_len(p, cur.b);
       const VisiblePages vis = seq_pages(p, n);
@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             if (!ok) {
               abort_s = 1;
             } else {
+              sent = cnt + 1;
               unsigned char* dst = ring + (size_t)st * Gm::STAGE_BYTES;
               mbar_arrive_expect_tx(&full[st], Gm::STAGE_BYTES);
 #pragma unroll
@@ -257,6 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         }
       }
     }
+    // after a wait that ran out: the copies in flight land before the CTA ends
+    if (lane == 0 && abort_s)
+      for (int i = max(0, sent - Gm::STAGES); i < sent; ++i) mbar_wait_bounded(&full[i % Gm::STAGES], (i / Gm::STAGES) & 1);
     return;
   }
 
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     for (int v = pb; v < pe; ++v, ++cnt) {
       if ((cnt % kGroups) != grp) continue;
       const int st = cnt % Gm::STAGES;
-      if (alive && !mbar_wait_bounded(&full[st], (cnt / Gm::STAGES) & 1)) {
+      if (alive && !__all_sync(0xffffffffu, mbar_wait_bounded(&full[st], (cnt / Gm::STAGES) & 1))) {
         alive = false;
         abort_s = 1;
         if (lane == 0) record_error(p.err, kDevWaitTimeout, (uint32_t)bh);
