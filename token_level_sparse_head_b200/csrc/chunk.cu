@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   extern __shared__ unsigned char smem_raw[];
   unsigned char* qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* ring = qs + 2 * Gm::Q_BUFS * Gm::TILE_BYTES;
-  __shared__ uint64_t full[ST], empty[ST], q_full[Gm::Q_BUFS], q_empty[Gm::Q_BUFS], s_full[2], s_read[2], p_ready[2], pv_done[2], half_full, half_free, drain;
+  __shared__ uint64_t full[ST], empty[ST], q_full[Gm::Q_BUFS], q_empty[Gm::Q_BUFS];
+  __shared__ uint64_t s_full[2], s_read[2], p_ready[2], pv_done[2], half_full, half_free, drain;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int stop_s;
   __shared__ const ChunkTask* volatile list_s;
@@ -464,88 +465,88 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     int cnt = 0, seg = 0;  // blocks and Q tiles asked for
     bool live = true;
     for (int w = 0; w < waves; ++w) {
-    Place c = share_s[w].at;
-    const long long u1 = share_s[w].u1;
-    for (long long u = share_s[w].u0; u < u1 && live;) {
-      const ChunkTask t = list[c.task];
-      const int be = (int)min((long long)t.blocks, c.block + (u1 - u)), units_here = be - c.block;
-      const bool one = t.ntok <= p.tok_tile;
-      const VisiblePages vis = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks);
-      // rows of 32 pages, page v with lane v % 32, looked up 16 at a time
-      int row = 0, have = c.block * (one ? 4 : 2);
-      auto push = [&](const CUtensorMap* map, int v) {
-        while (v + 2 > have) {
-          const int w = have + ((lane - have) & 31);
-          if (w < have + 16) {
-            row = p.row_end;
-            const int lp = vis.page(w);
-            if (w < vis.nv) {
-              if (p.paged) {
-                const int pg = p.page_table[(size_t)t.b * p.max_pages + lp];
-                if (pg < 0 || pg >= p.num_pages) record_error(p.err, kDevBadPage, (uint32_t)t.b);
-                else row = (pg * p.Hkv + c.h) * kPage;
-              } else {
-                row = (t.b * p.Hkv + c.h) * p.cap + lp * kPage;
+      Place c = share_s[w].at;
+      const long long u1 = share_s[w].u1;
+      for (long long u = share_s[w].u0; u < u1 && live;) {
+        const ChunkTask t = list[c.task];
+        const int be = (int)min((long long)t.blocks, c.block + (u1 - u)), units_here = be - c.block;
+        const bool one = t.ntok <= p.tok_tile;
+        const VisiblePages vis = visible_pages(t.pos0, t.pos0 + t.ntok - 1, p.window, p.sinks);
+        // rows of 32 pages, page v with lane v % 32, looked up 16 at a time
+        int row = 0, have = c.block * (one ? 4 : 2);
+        auto push = [&](const CUtensorMap* map, int v) {
+          while (v + 2 > have) {
+            const int ahead = have + ((lane - have) & 31);
+            if (ahead < have + 16) {
+              row = p.row_end;
+              const int lp = vis.page(ahead);
+              if (ahead < vis.nv) {
+                if (p.paged) {
+                  const int pg = p.page_table[(size_t)t.b * p.max_pages + lp];
+                  if (pg < 0 || pg >= p.num_pages) record_error(p.err, kDevBadPage, (uint32_t)t.b);
+                  else row = (pg * p.Hkv + c.h) * kPage;
+                } else {
+                  row = (t.b * p.Hkv + c.h) * p.cap + lp * kPage;
+                }
+              }
+            }
+            have += 16;
+          }
+          const int y0 = __shfl_sync(0xffffffffu, row, v & 31), y1 = __shfl_sync(0xffffffffu, row, (v + 1) & 31);
+          if (lane == 0 && live) {
+            const int st = cnt % ST;
+            live = cnt < ST || wait_live(&empty[st], ((cnt / ST) & 1) ^ 1, &stop_s);
+            if (live) {
+              unsigned char* dst = ring + (size_t)st * Gm::TILE_BYTES;
+              mbar_arrive_expect_tx(&full[st], Gm::TILE_BYTES);
+#pragma unroll
+              for (int hf = 0; hf < Gm::HALVES; ++hf) {
+                tma_2d(dst + hf * Gm::HALF_BYTES, map, hf * 64, y0, &full[st]);
+                tma_2d(dst + hf * Gm::HALF_BYTES + kPage * 128, map, hf * 64, y1, &full[st]);
               }
             }
           }
-          have += 16;
-        }
-        const int y0 = __shfl_sync(0xffffffffu, row, v & 31), y1 = __shfl_sync(0xffffffffu, row, (v + 1) & 31);
-        if (lane == 0 && live) {
-          const int st = cnt % ST;
-          live = cnt < ST || wait_live(&empty[st], ((cnt / ST) & 1) ^ 1, &stop_s);
-          if (live) {
-            unsigned char* dst = ring + (size_t)st * Gm::TILE_BYTES;
-            mbar_arrive_expect_tx(&full[st], Gm::TILE_BYTES);
+          live = __shfl_sync(0xffffffffu, live, 0);
+          if (live) ++cnt;
+        };
+        auto load_q = [&] {
+          const int qb = seg % Gm::Q_BUFS;
+          if (lane == 0 && live) {
+            live = seg < Gm::Q_BUFS || wait_live(&q_empty[qb], ((seg / Gm::Q_BUFS) & 1) ^ 1, &stop_s);
+            if (live) {
+              const int box = p.G * p.tok_tile * 128;
+              mbar_arrive_expect_tx(&q_full[qb], (one ? 1 : 2) * Gm::HALVES * box);
+              for (int i = 0; i < (one ? 1 : 2); ++i)
 #pragma unroll
-            for (int hf = 0; hf < Gm::HALVES; ++hf) {
-              tma_2d(dst + hf * Gm::HALF_BYTES, map, hf * 64, y0, &full[st]);
-              tma_2d(dst + hf * Gm::HALF_BYTES + kPage * 128, map, hf * 64, y1, &full[st]);
+                for (int hf = 0; hf < Gm::HALVES; ++hf)
+                  tma_3d(qs + (2 * qb + i) * Gm::TILE_BYTES + hf * Gm::HALF_BYTES, &p.qmap, hf * 64, c.h * p.G,
+                         t.tok0 + i * p.tok_tile, &q_full[qb]);
             }
           }
-        }
-        live = __shfl_sync(0xffffffffu, live, 0);
-        if (live) ++cnt;
-      };
-      auto load_q = [&] {
-        const int qb = seg % Gm::Q_BUFS;
-        if (lane == 0 && live) {
-          live = seg < Gm::Q_BUFS || wait_live(&q_empty[qb], ((seg / Gm::Q_BUFS) & 1) ^ 1, &stop_s);
-          if (live) {
-            const int box = p.G * p.tok_tile * 128;
-            mbar_arrive_expect_tx(&q_full[qb], (one ? 1 : 2) * Gm::HALVES * box);
-            for (int i = 0; i < (one ? 1 : 2); ++i)
-#pragma unroll
-              for (int hf = 0; hf < Gm::HALVES; ++hf)
-                tma_3d(qs + (2 * qb + i) * Gm::TILE_BYTES + hf * Gm::HALF_BYTES, &p.qmap, hf * 64, c.h * p.G,
-                       t.tok0 + i * p.tok_tile, &q_full[qb]);
+          live = __shfl_sync(0xffffffffu, live, 0);
+          if (live) ++seg;
+        };
+        // the first keys do not wait for the room that Q waits for
+        if (one) {
+          push(&p.kmap, 4 * c.block);
+          push(&p.kmap, 4 * c.block + 2);
+          load_q();
+          for (int j = c.block; j < be; ++j)
+            for (int x = 0; x < 2; ++x) {
+              if (j + 1 < be) push(&p.kmap, 4 * j + 4 + 2 * x);
+              push(&p.vmap, 4 * j + 2 * x);
+            }
+        } else {
+          push(&p.kmap, 2 * c.block);
+          load_q();
+          for (int j = c.block; j < be; ++j) {
+            if (j + 1 < be) push(&p.kmap, 2 * j + 2);
+            push(&p.vmap, 2 * j);
           }
         }
-        live = __shfl_sync(0xffffffffu, live, 0);
-        if (live) ++seg;
-      };
-      // the first keys do not wait for the room that Q waits for
-      if (one) {
-        push(&p.kmap, 4 * c.block);
-        push(&p.kmap, 4 * c.block + 2);
-        load_q();
-        for (int j = c.block; j < be; ++j)
-          for (int x = 0; x < 2; ++x) {
-            if (j + 1 < be) push(&p.kmap, 4 * j + 4 + 2 * x);
-            push(&p.vmap, 4 * j + 2 * x);
-          }
-      } else {
-        push(&p.kmap, 2 * c.block);
-        load_q();
-        for (int j = c.block; j < be; ++j) {
-          if (j + 1 < be) push(&p.kmap, 2 * j + 2);
-          push(&p.vmap, 2 * j);
-        }
+        u += units_here;
+        next_task(c, tasks);
       }
-      u += units_here;
-      next_task(c, tasks);
-    }
     }
     // after a wait that ran out: the copies in flight land before the CTA ends
     if (lane == 0 && !live) {
@@ -554,35 +555,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- matrix instructions
-    {
-      // The scores' buffer goes back and forth between this warp and the softmax: what does not
-      // depend on a wait is done before it.
-      const uint32_t lead = elect_lane();
-      constexpr uint32_t kFormS = mma_form(kTile, false), kFormO = mma_form(D, true);
-      const uint64_t qd = operand(smem_u32(qs), 16), kd = operand(smem_u32(ring), 16), vd = operand(smem_u32(ring), Gm::HALF_BYTES);
-      constexpr uint32_t kStep = Gm::TILE_BYTES >> 4;
-      int seg = 0;
-      Ring r = {0, 0}, k, v;
-      uint32_t ph_p = 0, ph_read = 1;  // parity of the scores' reads: the first use of a buffer waits for none
-      bool live = true;
-      auto scores = [&](int x, bool one) {  // S = Q K^T for warpgroup x, K in ring place k
-        const int buf = Gm::S_BUFS == 1 ? 0 : x;
-        const uint64_t a = qd + (2 * (seg % Gm::Q_BUFS) + (one ? 0 : x)) * kStep, b = kd + k.st * kStep;
-        live = live && wait_warp(&full[k.st], k.ph, &stop_s);
-        live = live && wait_warp(&s_read[buf], ph_read, &stop_s);  // the scores that were there have been read
-        if (Gm::S_BUFS == 1 || x == 1) ph_read ^= 1;
-        if (!live) return;
-        tc_fence_after();
+    // The scores' buffer goes back and forth between this warp and the softmax: what does not
+    // depend on a wait is done before it.
+    const uint32_t lead = elect_lane();
+    constexpr uint32_t kFormS = mma_form(kTile, false), kFormO = mma_form(D, true);
+    const uint64_t qd = operand(smem_u32(qs), 16), kd = operand(smem_u32(ring), 16), vd = operand(smem_u32(ring), Gm::HALF_BYTES);
+    constexpr uint32_t kStep = Gm::TILE_BYTES >> 4;
+    int seg = 0;
+    Ring r = {0, 0}, k, v;
+    uint32_t ph_p = 0, ph_read = 1;  // parity of the scores' reads: the first use of a buffer waits for none
+    bool live = true;
+    auto scores = [&](int x, bool one) {  // S = Q K^T for warpgroup x, K in ring place k
+      const int buf = Gm::S_BUFS == 1 ? 0 : x;
+      const uint64_t a = qd + (2 * (seg % Gm::Q_BUFS) + (one ? 0 : x)) * kStep, b = kd + k.st * kStep;
+      live = live && wait_warp(&full[k.st], k.ph, &stop_s);
+      live = live && wait_warp(&s_read[buf], ph_read, &stop_s);  // the scores that were there have been read
+      if (Gm::S_BUFS == 1 || x == 1) ph_read ^= 1;
+      if (!live) return;
+      tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          constexpr int kHalf = Gm::HALF_BYTES >> 4;
-          const uint32_t o = (i >> 2) * kHalf + (i & 3) * 2;
-          mma_ss(tmem + Gm::COL_S + buf * kTile, a + o, b + o, kFormS, i > 0, lead);
-        }
-        tc_commit(&s_full[x], lead);
-        if (one || x == 1) tc_commit(&empty[k.st], lead);
-      };
-      for (int w = 0; w < waves; ++w) {
+      for (int i = 0; i < D / 16; ++i) {
+        constexpr int kHalf = Gm::HALF_BYTES >> 4;
+        const uint32_t o = (i >> 2) * kHalf + (i & 3) * 2;
+        mma_ss(tmem + Gm::COL_S + buf * kTile, a + o, b + o, kFormS, i > 0, lead);
+      }
+      tc_commit(&s_full[x], lead);
+      if (one || x == 1) tc_commit(&empty[k.st], lead);
+    };
+    for (int w = 0; w < waves; ++w) {
       Place c = share_s[w].at;
       const long long u1 = share_s[w].u1;
       for (long long u = share_s[w].u0; u < u1 && live; ++seg) {
@@ -623,11 +623,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         u += n;
         next_task(c, tasks);
       }
-      }
-      // every product has left shared and tensor memory before they are given back
-      tc_commit(&drain, lead);
-      mbar_wait_bounded(&drain, 0);
     }
+    // every product has left shared and tensor memory before they are given back
+    tc_commit(&drain, lead);
+    mbar_wait_bounded(&drain, 0);
     __syncwarp();
   } else if (warp < 8) {
     // ---------------------------------------------------------------- softmax and output
