@@ -12,8 +12,8 @@
 // two, with lower numbers; segments are handed out by a counter, lower ones first, and none waits
 // before it has set its flag, so every wait ends.  The reads and writes of all segments are thus
 // in flight together; a CTA that went through a column slice of all rows in order, with no flags,
-// took 581 us for the 1.2 GB of a batch of 16 (8K to 128K rows, an eighth kept), this form 265 us
-// (4.7 TB/s); for one sequence of 32K 28.8 against 14.1 us.
+// took 581 us for the 1.2 GB of a batch of 16 (8K to 128K rows, an eighth kept), this form 256 us
+// (4.9 TB/s); for one sequence of 32K 28.8 against 13 us.
 #include "sas_device.cuh"
 #include "sas_kernels.h"
 
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
   __syncthreads();
 
   // ---- read ----
-  uint4 kv[2][PER], pj[PROJ];
+  uint4 kv[2][PER] = {}, pj[PROJ] = {};
 #pragma unroll
   for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -200,12 +200,18 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
     w = ld_ordered(p.weights + row0 + idx_s[tid]);
     if (p.log_g != nullptr) g = ld_ordered(p.log_g + row0 + idx_s[tid]);
   }
-  __syncthreads();
+  // A barrier that takes what was loaded as its input: no load is still on its way behind it.
+  uint32_t x = __float_as_uint(w) ^ __float_as_uint(g);
+#pragma unroll
+  for (int u = 0; u < PER; ++u) x ^= kv[0][u].x ^ kv[0][u].w ^ kv[1][u].x ^ kv[1][u].w;
+#pragma unroll
+  for (int u = 0; u < PROJ; ++u) x ^= pj[u].x ^ pj[u].w;
+  __syncthreads_or((int)x);
 
   // ---- the rows to be written may be the sources of this segment or of earlier ones ----
   uint32_t* flag = p.flags + (size_t)bh * p.segs;
   if (tid == 0) {
-    __threadfence();
+    // release: the reads of all threads before the barrier come before the flag
     st_release(flag + sg, 1u);
     go_s = 1;
     // rows j0 .. j0 + 63 are the sources of at most 64 kept rows, from first_s on
@@ -217,7 +223,6 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
           go_s = 0;
           break;
         }
-    __threadfence();
   }
   __syncthreads();
   if (!go_s) return;
