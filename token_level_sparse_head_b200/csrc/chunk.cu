@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const uint64_t qd = operand(smem_u32(qs), 16), kd = operand(smem_u32(ring), 16), vd = operand(smem_u32(ring), Gm::HALF_BYTES);
     constexpr uint32_t kStep = Gm::TILE_BYTES >> 4;
     int seg = 0;
-    Ring r = {0, 0}, k, v;
+    Ring r = {0, 0}, k = {0, 0}, v = {0, 0};
     uint32_t ph_p = 0, ph_read = 1;  // parity of the scores' reads: the first use of a buffer waits for none
     bool live = true;
     auto scores = [&](int x, bool one) {  // S = Q K^T for warpgroup x, K in ring place k
