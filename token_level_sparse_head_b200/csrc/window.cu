@@ -17,7 +17,7 @@
 // the second product as three bf16 terms of 8 bits each, which hold its 24 bits exactly, because
 // the output is fp32: one bf16 term would be off by up to 2^-8, two by 2^-16.
 // Measured (8 KV heads, d = 128): window 4096 at B = 16 52 us, 5.2 TB/s; whole caches of 4 x 64K rows
-// with weights 203 us, 5.4 TB/s, of which the weights' own pass takes 16; window 1024 at B = 1 9.2 us,
+// with weights 200 us, 5.4 TB/s, of which the weights' own pass takes 13; window 1024 at B = 1 9.2 us,
 // where the chain of page, products and join counts and not the bytes.
 #include "sas_device.cuh"
 #include "sas_kernels.h"
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 }
 
 // weights[b,h,j] += sum_g 2^(z - lse2).  A thread takes kWeightRows visible rows, all of whose loads
-// are in flight at once (one row a thread: 17 us for 4 x 64K rows of 8 heads, four: 15.7 us).
+// are in flight at once (one row a thread: 17 us for 4 x 64K rows of 8 heads, four: 12.8 us).
 constexpr int kWeightThreads = 256, kWeightRows = 4;
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_constant__ WindowParams p) {
   pdl_wait();
@@ -563,6 +563,9 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_co
     const int at = vis.page(vr / kPage) * kPage + vr % kPage;
     if (at < n && (p.window <= 0 || at >= vis.first || at < p.sinks)) j[i] = at;
   }
+  float was[kWeightRows];
+#pragma unroll
+  for (int i = 0; i < kWeightRows; ++i) was[i] = j[i] >= 0 ? w[j[i]] : 0.f;
   if (p.G % 4 == 0) {
     for (int g = 0; g < p.G; g += 4) {
       const float l0 = ls[g], l1 = ls[g + 1], l2 = ls[g + 2], l3 = ls[g + 3];
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_co
   }
 #pragma unroll
   for (int i = 0; i < kWeightRows; ++i)
-    if (j[i] >= 0) w[j[i]] += s[i];
+    if (j[i] >= 0) w[j[i]] = was[i] + s[i];
 }
 
 template <int D, int NT>
