@@ -998,8 +998,12 @@ void plan_chunk(ChunkParams& p) {
   p.tok_tile = kTile / p.G;
   p.slots = p.n_new / (2 * p.tok_tile) + p.B;
   p.own_plan = p.slots <= kOwnPlanSlots ? 1 : 0;
-  // More than one wave only where some sequence can have several tasks.
-  p.waves_max = p.n_new > 2 * p.tok_tile ? (p.Hkv < kChunkMaxWaves ? p.Hkv : kChunkMaxWaves) : 1;
+  // More than one wave only where some sequence can have several tasks and the cache can exceed a wave.
+  const long long bytes = (p.paged ? (long long)p.num_pages * kPage : (long long)p.B * p.cap) * p.Hkv * p.d * 4;
+  const long long most = 1 + bytes / kLiveBytes;
+  p.waves_max = p.Hkv < kChunkMaxWaves ? p.Hkv : kChunkMaxWaves;
+  if (most < p.waves_max) p.waves_max = (int)most;
+  if (p.n_new <= 2 * p.tok_tile) p.waves_max = 1;
 }
 
 size_t chunk_workspace_bytes(const ChunkParams& p) {
