@@ -349,9 +349,10 @@ sas_status do_select(const sas_shape* s, const void* q, const float* M, const vo
 
 sas_status do_attend(const sas_shape* s, const void* q, const void* K, const void* V, const int32_t* page_table,
                      const int32_t* seqlens, const int32_t* idx, const int32_t* k, int32_t count_max,
-                     float lambda, const float* log_g, float* out, void* ws, cudaStream_t st) {
+                     float lambda, const float* log_g, float* out, bool first, void* ws, cudaStream_t st) {
   sas::AttendParams a = attend_plan(s, count_max, idx == nullptr);
   bind_workspace(a, ws);
+  a.first = first ? 1 : 0;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.K = static_cast<const __nv_bfloat16*>(K);
   a.V = static_cast<const __nv_bfloat16*>(V);
@@ -521,6 +522,7 @@ sas_status sas_select_from_scores(const sas_shape* shape, const int32_t* seqlens
   SelectPlan pl;
   SAS_TRY(plan_selection(shape, nullptr, nullptr, nullptr, nullptr, seqlens, k, k_max, 0.0f, nullptr, idx_out,
                          nullptr, workspace, &pl));
+  pl.sl.first = 1;
   return run_select(pl, static_cast<cudaStream_t>(stream));
 }
 
@@ -540,7 +542,7 @@ sas_status sas_sparse_attention(const sas_shape* shape, const void* q, const voi
   if (lambda != 0.0f) SAS_TRY(check_ptr(log_g, "log_g"));
   SAS_TRY(check_ptr(workspace, "workspace"));
   if (ws_bytes < sas_decode_workspace_bytes(shape, k_max)) return fail(SAS_ERR_INVALID_ARG, "workspace too small");
-  return do_attend(shape, q, K, V, page_table, seqlens, idx, k, k_max, lambda, log_g, out, workspace,
+  return do_attend(shape, q, K, V, page_table, seqlens, idx, k, k_max, lambda, log_g, out, true, workspace,
                    static_cast<cudaStream_t>(stream));
 }
 
@@ -565,7 +567,7 @@ sas_status sas_decode_step(const sas_shape* shape, const void* q, const float* M
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   SAS_TRY(do_select(shape, q, M, Kproj, page_table, seqlens, k, k_max, lambda, log_g, idx_out, nullptr,
                     workspace, st));
-  return do_attend(shape, q, K, V, page_table, seqlens, idx_out, k, k_max, lambda, log_g, out, workspace, st);
+  return do_attend(shape, q, K, V, page_table, seqlens, idx_out, k, k_max, lambda, log_g, out, false, workspace, st);
 }
 
 sas_status sas_dense_decode(const sas_shape* shape, const void* q, const void* K, const void* V,
@@ -579,7 +581,7 @@ sas_status sas_dense_decode(const sas_shape* shape, const void* q, const void* K
   SAS_TRY(check_cache_ptrs(shape, page_table, seqlens));
   SAS_TRY(check_ptr(workspace, "workspace"));
   if (ws_bytes < sas_dense_workspace_bytes(shape)) return fail(SAS_ERR_INVALID_ARG, "workspace too small");
-  return do_attend(shape, q, K, V, page_table, seqlens, nullptr, nullptr, cap_of(shape), 0.0f, nullptr, out,
+  return do_attend(shape, q, K, V, page_table, seqlens, nullptr, nullptr, cap_of(shape), 0.0f, nullptr, out, true,
                    workspace, static_cast<cudaStream_t>(stream));
 }
 
@@ -974,7 +976,7 @@ sas_status sas_decode_step_static_scratch(const sas_shape* shape, const void* q,
   const cudaError_t e = cudaMemsetAsync(ws, 0, L.partials, st);
   if (e != cudaSuccess) return cuda_fail(e, "clearing the static scratch");
   SAS_TRY(do_select(shape, q, M, Kproj, page_table, seqlens, k, k_max, lambda, log_g, idx_out, nullptr, ws, st));
-  return do_attend(shape, q, K, V, page_table, seqlens, idx_out, k, k_max, lambda, log_g, out, ws, st);
+  return do_attend(shape, q, K, V, page_table, seqlens, idx_out, k, k_max, lambda, log_g, out, false, ws, st);
 }
 
 }  // extern "C"

@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
   const int b = bh / p.Hkv, h = bh % p.Hkv;
   const int bhz = bh * p.ngz + gz;
 
+  if (DENSE || p.first) pdl_wait();
   int n = p.seqlens[b];
   if (n < 0 || n > p.cap) {
     if (split == 0 && tid == 0 && h == 0 && gz == 0) record_error(p.err, kDevBadSeqlen, (uint32_t)b);

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
   constexpr int PROJ = kSeg * 128 / 16 / kMoveThreads;       // of the widest projected row
   __shared__ long long src_s[kSeg], dst_s[kSeg];
   __shared__ int idx_s[kSeg + 1], ticket_s, first_s, go_s;
-  // No early trigger: this kernel writes the lengths, which the next kernel may read before its wait.
+  // No early trigger: all that the next call's first kernel could do before its wait is set up barriers.
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31;
   if (tid == 0) ticket_s = (int)atomicAdd(p.ticket, 1u);

@@ -84,6 +84,12 @@ __device__ __forceinline__ VisiblePages visible_pages(int p_lo, int p_hi, int wi
 // the next kernel may start its independent prologue while this one runs.  Once a kernel has
 // passed pdl_wait() every earlier kernel on the stream has completed (each of them waited for
 // its own predecessor before triggering).  Both are no-ops for a launch without the attribute.
+//
+// The first kernel of a call waits before it reads anything, lengths and budgets among it: the
+// kernel before it is another call's, or the caller's own, and may have written any of them (an
+// eviction writes the lengths).  Only the wait makes those writes visible; that its CTAs have
+// ended does not.  A later kernel of the call may read the call's inputs before its wait, because
+// all CTAs of the call's first kernel had passed theirs when it was launched.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -69,6 +69,7 @@ struct SelectParams {
   int chunk;                   // max positions per CTA (multiple of 512)
   int cand_cap;                // candidate list capacity per CTA
   int off_hist, off_ctl, smem_bytes;
+  int first;                   // the selection is the call's first kernel
 };
 // Chooses cluster size and chunk for a shape; returns false if unsupported.
 bool plan_select(SelectParams& p, int num_sms);
@@ -111,6 +112,7 @@ struct AttendParams {
   int max_splits;              // splits the workspace holds partials for (>= splits)
   int smem_bytes;
   int sms;                     // SMs of the device (launch-time re-split)
+  int first;                   // the attention is the call's first kernel
 };
 // Split plan for `count_max` index entries per head (dense: every cached row); a pure function
 // of the arguments, which sizes the workspace.  launch_attend may re-split the work (up to

@@ -199,6 +199,10 @@ __global__ void __launch_bounds__(Cfg<R, GATED, KP8>::kThreads, 1) score_kernel(
   }
   for (int i = tid; i < C::kBins; i += C::kThreads) S.hist[i] = 0u;
 
+  // Everything below depends on the lengths, which the kernel before this one may have written.
+  pdl_wait();
+  pdl_trigger();
+
   // ---- this CTA's share of the block list (warp 0) ----
   if (warp == 0) {
     // per-lane block counts of sequences lane, lane + 32, ...; the first 32 are kept
@@ -254,10 +258,6 @@ __global__ void __launch_bounds__(Cfg<R, GATED, KP8>::kThreads, 1) score_kernel(
     }
   }
   __syncthreads();
-  // The projected cache (appended to by the previous kernel), the keys, the histograms and the
-  // error word are touched only from here on.
-  pdl_wait();
-  pdl_trigger();
   const Plan pl = S.plan;
 
   bool waited_ok = true;

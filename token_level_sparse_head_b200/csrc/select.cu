@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(THREADS, 1) select_topk_kernel(const SelectPar
   const int bh = blockIdx.y;
   const int b = bh / p.Hkv;
 
+  if (p.first) pdl_wait();
   // per-sequence values (range errors were recorded by the score kernel)
   int n = p.seqlens[b];
   if (n < 0 || n > p.cap) n = 0;
