@@ -231,8 +231,10 @@ sas_status sas_gather_selected(const sas_shape* shape, const void* K, const void
  *     counts them: token t of the chunk sits at position N_b - T_b + t.
  *   n_new: rows of the batch's arrays on the host's side, q_start[B] <= n_new.  Rows outside
  *     every sequence are neither read for a result nor written.
- * A sequence whose q_start entries are out of order, out of [0, n_new], or that has more new
- * tokens than N_b is skipped (its outputs stay as they were) and sets the error word.
+ * A sequence is skipped (its outputs and cache rows stay as they were) and sets the error word
+ * whose q_start[b] is below 0 or below an earlier entry of q_start, whose
+ * q_start[b+1] is below q_start[b] or above n_new, that has more new tokens than N_b, or whose
+ * N_b lies outside the cache.  Sequences that are not skipped never share a row of the batch.
  * Token strides (q_stride, kv_stride) are in elements between consecutive tokens, multiples
  * of 8, so that rows of a fused projection can be passed as they are.
  *

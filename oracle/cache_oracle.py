@@ -28,6 +28,19 @@ def visible(p, n, window, sinks):
     return m
 
 
+def chunk_errors(q_start, seqlens, n_new, cap):
+    """Why each sequence of a chunk batch is skipped: 0 (taken), 1 (its length), 6 (its rows)."""
+    why, top = [], None
+    for b, n in enumerate(seqlens):
+        s0, s1 = int(q_start[b]), int(q_start[b + 1])
+        top = s0 if top is None else max(top, s0)
+        if not 0 <= n <= cap:
+            why.append(1)
+        else:
+            why.append(0 if 0 <= s0 and top == s0 <= s1 <= n_new and s1 - s0 <= n else 6)
+    return why
+
+
 def append_chunk(K, V, K_new, V_new, q_start, seqlens, page_table):
     """K, V updated copies: rows N_b - T_b .. N_b - 1 of every (b, h) from the chunk."""
     K, V = K.copy(), V.copy()

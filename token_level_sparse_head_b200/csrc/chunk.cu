@@ -216,25 +216,21 @@ __device__ __forceinline__ void make_plan(const ChunkParams& p, ChunkTask* tasks
   const int span = 2 * p.tok_tile;
   int base = 0;
   if (tid == 0) S.keys = 0;
-  __syncthreads();
+  const bool ordered = starts_in_order<THREADS>(p.q_start, p.B);
+  LargestStart largest;
   for (int b0 = 0; b0 < p.B; b0 += THREADS) {
     const int b = b0 + tid;
     int cnt = 0;
     if (b < p.B) {
-      const int s0 = p.q_start[b], s1 = p.q_start[b + 1], n = p.seqlens[b];
-      if (n < 0 || n > p.cap) record_error(p.err, kDevBadSeqlen, (uint32_t)b);
-      else if (s0 < 0 || s1 < s0 || s1 > p.n_new || s1 - s0 > n) record_error(p.err, kDevBadChunk, (uint32_t)b);
+      const int s0 = p.q_start[b], s1 = p.q_start[b + 1];
+      const uint32_t why = chunk_error(s0, s1, ordered ? s0 : largest.upto(p.q_start, b), p.seqlens[b], p.n_new, p.cap);
+      if (why != kDevOk) record_error(p.err, why, (uint32_t)b);
       else cnt = (s1 - s0 + span - 1) / span;
     }
     int total;
-    int end = block_scan<THREADS>(cnt, S.sum, total);
-    // sequences that overlap could exceed the slots: such a sequence is skipped
-    if (base + end > p.slots && cnt > 0) {
-      record_error(p.err, kDevBadChunk, (uint32_t)b);
-      end = p.slots - base;
-    }
+    const int end = block_scan<THREADS>(cnt, S.sum, total);
     if (tid == 0) S.off[0] = 0;
-    S.off[tid + 1] = min(end, p.slots - base);
+    S.off[tid + 1] = end;  // sequences that are taken do not overlap, so their tasks fit the slots
     __syncthreads();
     for (int i = warp; i < min(THREADS, p.B - b0); i += THREADS / 32) {
       const int k0 = S.off[i], k1 = S.off[i + 1];
@@ -256,7 +252,7 @@ __device__ __forceinline__ void make_plan(const ChunkParams& p, ChunkTask* tasks
       }
     }
     __syncthreads();
-    base = min(base + total, p.slots);
+    base += total;
   }
   long long units = 0;
   for (int k0 = 0; k0 < base; k0 += THREADS) {

@@ -61,6 +61,30 @@ __device__ __forceinline__ SeqSelection seq_selection(int kb, int n) {
   return s;
 }
 
+// ----------------------------------------------------------------------------- chunk batches
+// Whether no entry of q_start [B+1] is smaller than the one before it.  The whole CTA; a barrier.
+template <int THREADS>
+__device__ __forceinline__ bool starts_in_order(const int32_t* q_start, int B) {
+  bool falls = false;
+  for (int b = threadIdx.x; b < B; b += THREADS) falls |= q_start[b + 1] < q_start[b];
+  return !__syncthreads_or(falls);
+}
+// The largest of q_start[0 .. b] for growing b; looked at only where some entry is out of order.
+struct LargestStart {
+  int next = 0, top = INT32_MIN;
+  __device__ __forceinline__ int upto(const int32_t* q_start, int b) {
+    for (; next <= b; ++next) top = max(top, q_start[next]);
+    return top;
+  }
+};
+// Why sequence b's chunk is skipped, or kDevOk.  top: the largest of q_start[0 .. b].  Sequences
+// that are taken do not overlap: none starts below an earlier entry.
+__device__ __forceinline__ uint32_t chunk_error(int s0, int s1, int top, int n, int n_new, int cap) {
+  if (n < 0 || n > cap) return kDevBadSeqlen;
+  if (s0 < 0 || s0 < top || s1 < s0 || s1 > n_new || s1 - s0 > n) return kDevBadChunk;
+  return kDevOk;
+}
+
 // ----------------------------------------------------------------------------- visible pages
 // The 64-row pages that the positions p_lo .. p_hi of one sequence see: the sinks' pages that lie
 // before the window, then the window's.  Virtual page v of nv is page(v) of the sequence.
