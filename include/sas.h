@@ -231,8 +231,8 @@ sas_status sas_gather_selected(const sas_shape* shape, const void* K, const void
  *     counts them: token t of the chunk sits at position N_b - T_b + t.
  *   n_new: rows of the batch's arrays on the host's side, q_start[B] <= n_new.  Rows outside
  *     every sequence are neither read for a result nor written.
- * A sequence is skipped (its outputs and cache rows stay as they were) and sets the error word
- * whose q_start[b] is below 0 or below an earlier entry of q_start, whose
+ * A sequence is skipped (its outputs and cache rows stay as they were) and sets the error word,
+ * in every call alike, whose q_start[b] is below 0 or below an earlier entry of q_start, whose
  * q_start[b+1] is below q_start[b] or above n_new, that has more new tokens than N_b, or whose
  * N_b lies outside the cache.  Sequences that are not skipped never share a row of the batch.
  * Token strides (q_stride, kv_stride) are in elements between consecutive tokens, multiples

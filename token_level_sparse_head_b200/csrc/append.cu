@@ -1,10 +1,11 @@
 // Rows of a chunk of new tokens into the caches: K, V and the projected rows (sm_100a).
 //
 // Token t of the batch belongs to the sequence b with q_start[b] <= t < q_start[b+1] and sits at
-// position N_b - T_b + (t - q_start[b]).  Per token and KV head the call copies 2 d bf16 values and
-// computes r dot products of length d in fp32, in the summation order of the projection build (8
-// partial sums over consecutive blocks of d/8 channels, in channel order, combined as
-// ((p0+p1)+(p2+p3))+((p4+p5)+(p6+p7))), so a row is the same bits whichever call wrote it.
+// position N_b - T_b + (t - q_start[b]); every CTA sees for itself whether q_start is in order.  Per
+// token and KV head the call copies 2 d bf16 values and computes r dot products of length d in fp32,
+// in the summation order of the projection build (8 partial sums over consecutive blocks of d/8
+// channels, in channel order, combined as ((p0+p1)+(p2+p3))+((p4+p5)+(p6+p7))), so a row is the same
+// bits whichever call wrote it.
 //
 // Two kernels, by the number of (token, head) pairs:
 //   token_kernel  one CTA per pair, 8 threads per output: few tokens, where latency counts;
@@ -25,32 +26,42 @@
 namespace sas {
 namespace {
 
-// Sequence and cache row of token t; row < 0 if the token belongs to nobody or a check failed.
-__device__ __forceinline__ long long token_row(const AppendParams& p, int t, int h) {
-  int lo = 0, hi = p.B;  // largest b in [0, B) with q_start[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.q_start[mid] <= t) lo = mid; else hi = mid;
+// Cache row of token t; -1 if the token belongs to nobody or to a sequence that is skipped, -2 - b
+// if its page (of sequence b) lies outside the cache.
+// ordered: no entry of q_start is smaller than the one before it, so the last start that is not
+// above t is t's.  Otherwise the first sequence that may be taken and holds t, in order.
+__device__ __forceinline__ long long token_row(const AppendParams& p, bool ordered, int t, int h) {
+  int b = 0;
+  LargestStart largest;
+  if (ordered) {
+    int hi = p.B;  // largest b in [0, B) with q_start[b] <= t
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (p.q_start[mid] <= t) b = mid; else hi = mid;
+    }
+  } else {
+    while (b < p.B - 1 && !(p.q_start[b] >= largest.upto(p.q_start, b) && p.q_start[b] <= t && t < p.q_start[b + 1])) ++b;
   }
-  const int b = lo, s0 = p.q_start[b], s1 = p.q_start[b + 1];
-  if (t < s0 || t >= s1) return -1;
-  const int n = p.seqlens[b];
-  if (n < 0 || n > p.cap) {
-    record_error(p.err, kDevBadSeqlen, (uint32_t)b);
-    return -1;
-  }
-  if (s0 < 0 || s1 > p.n_new || s1 - s0 > n) {
-    record_error(p.err, kDevBadChunk, (uint32_t)b);
-    return -1;
-  }
+  const int s0 = p.q_start[b], s1 = p.q_start[b + 1], n = p.seqlens[b];
+  if (t < s0 || t >= s1 || chunk_error(s0, s1, ordered ? s0 : largest.upto(p.q_start, b), n, p.n_new, p.cap) != kDevOk) return -1;
   const int pos = n - (s1 - s0) + (t - s0);
   if (!p.paged) return ((long long)b * p.Hkv + h) * p.cap + pos;
   const int pg = p.page_table[(size_t)b * p.max_pages + (pos >> 6)];
-  if (pg < 0 || pg >= p.num_pages) {
-    record_error(p.err, kDevBadPage, (uint32_t)b);
-    return -1;
-  }
+  if (pg < 0 || pg >= p.num_pages) return -2 - b;
   return ((long long)pg * p.Hkv + h) * 64 + (pos & 63);
+}
+__device__ __forceinline__ void record_row(const AppendParams& p, long long row) {
+  if (row < -1) record_error(p.err, kDevBadPage, (uint32_t)(-2 - row));
+}
+// Records why sequences are skipped, those without tokens among them; one CTA of the grid.
+template <int THREADS>
+__device__ __forceinline__ void record_skipped(const AppendParams& p, bool ordered) {
+  LargestStart largest;
+  for (int b = threadIdx.x; b < p.B; b += THREADS) {
+    const int s0 = p.q_start[b];
+    const uint32_t why = chunk_error(s0, p.q_start[b + 1], ordered ? s0 : largest.upto(p.q_start, b), p.seqlens[b], p.n_new, p.cap);
+    if (why != kDevOk) record_error(p.err, why, (uint32_t)b);
+  }
 }
 
 __device__ __forceinline__ unsigned char fp8_of(float a, float s) {
@@ -63,7 +74,8 @@ __global__ void __launch_bounds__(256) token_kernel(const AppendParams p) {
   pdl_trigger();
   const int t = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   __shared__ long long row_s;
-  if (threadIdx.x == 0) row_s = token_row(p, t, h);
+  // looked up as if q_start were in order, while the other threads see whether it is
+  if (threadIdx.x == 0) row_s = token_row(p, true, t, h);
   constexpr int BLK = D / 8;
   const int part = threadIdx.x & 7;
   const __nv_bfloat16* kn = p.K_new + (size_t)t * p.kv_stride + (size_t)h * D;
@@ -103,9 +115,17 @@ __global__ void __launch_bounds__(256) token_kernel(const AppendParams p) {
       out[pass] = a;
     }
   }
-  __syncthreads();
+  const bool ordered = starts_in_order<256>(p.q_start, p.B);
+  if (!ordered) {
+    if (threadIdx.x == 0) row_s = token_row(p, false, t, h);
+    __syncthreads();
+  }
+  if (blockIdx.x == 0) record_skipped<256>(p, ordered);
   const long long row = row_s;
-  if (row < 0) return;
+  if (row < 0) {
+    if (threadIdx.x == 0) record_row(p, row);
+    return;
+  }
   if (threadIdx.x < 2 * PPR)
     *reinterpret_cast<uint4*>((threadIdx.x < PPR ? p.K : p.V) + (size_t)row * D + (threadIdx.x % PPR) * 8) = piece;
   if (p.Kproj != nullptr && part == 0) {
@@ -149,7 +169,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(const AppendParam
   const int tiles = (p.n_new + kTileTokens - 1) / kTileTokens;
   constexpr int PPR = D / 8, PER = kTileTokens * PPR / kTileThreads;
   // A tile's keys are asked for, and its cache rows looked up, while the tile before is worked on.
-  auto ask = [&](int tile, int buf) {
+  auto ask_keys = [&](int tile, int buf) {
     const int t0 = tile * kTileTokens, nt = min(kTileTokens, p.n_new - t0);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -157,9 +177,15 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(const AppendParam
       if (t < nt) copy_async16(&S.K[buf][t][c * 16], p.K_new + (size_t)(t0 + t) * p.kv_stride + (size_t)h * D + c * 8);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    if (tid < kTileTokens) S.row[buf][tid] = tid < nt ? token_row(p, t0 + tid, h) : -1;
   };
-  ask(blockIdx.x, 0);
+  auto look_up = [&](int tile, int buf, bool ordered) {
+    const int t = tile * kTileTokens + tid;
+    if (tid >= kTileTokens) return;
+    const long long row = t < p.n_new ? token_row(p, ordered, t, h) : -1;
+    record_row(p, row);
+    S.row[buf][tid] = row;
+  };
+  ask_keys(blockIdx.x, 0);
   if (p.Kproj != nullptr) {
     // M[h] is [R][D]: a thread moves 4 channels of one output (outputs vary fastest over the
     // lanes, so that the transposed stores of a warp fall into different banks)
@@ -173,6 +199,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(const AppendParam
       S.Mt[c + 3][j] = m.w;
     }
   }
+  const bool ordered = starts_in_order<kTileThreads>(p.q_start, p.B);
+  look_up(blockIdx.x, 0, ordered);
+  if (blockIdx.x == 0 && h == 0) record_skipped<kTileThreads>(p, ordered);
   int buf = 0;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
     const int t0 = tile * kTileTokens, nt = min(kTileTokens, p.n_new - t0);
@@ -184,7 +213,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(const AppendParam
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    if (tile + (int)gridDim.x < tiles) ask(tile + gridDim.x, buf ^ 1);
+    if (tile + (int)gridDim.x < tiles) {
+      ask_keys(tile + gridDim.x, buf ^ 1);
+      look_up(tile + gridDim.x, buf ^ 1, ordered);
+    }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = tid + i * kTileThreads, t = e / PPR, c = e % PPR;
