@@ -20,6 +20,12 @@ def _tokens(x, heads: int, d: int, name: str):
     return size[0], step[0] if size[0] > 1 else heads * d
 
 
+def _other_layout(x, dtype, shape) -> bool:
+    """x is neither dense [shape] of dtype nor more of the same along the first axis."""
+    size = x.shape
+    return x.dtype is not dtype or not x.is_contiguous() or len(size) != len(shape) or size[1:] != shape[1:] or size[0] < shape[0]
+
+
 class DecodeSession:
     """Workspace + output buffers for repeated decode steps of one shape and budget bound.
 
@@ -33,6 +39,16 @@ class DecodeSession:
         self.shape = shape
         self.k_max = int(k_max)
         self.chunk_max = int(chunk)
+        # (name, type, extents) of what the calls around the step take; there may be more along the first axis
+        s, i32, f32, bf16 = shape, torch.int32, torch.float32, torch.bfloat16
+        self._rows = (s.num_pages, s.Hkv, s.page_size) if s.page_size else (s.B, s.Hkv, s.n_cap)
+        positions, heads = (s.B, s.Hkv, s.cap), (s.B, s.Hq, s.d)
+        self._starts, self._m = ("q_start", i32, (s.B + 1,)), ("M", f32, (s.Hkv, s.r, s.d))
+        self._cache = (("K", bf16, (*self._rows, s.d)), ("V", bf16, (*self._rows, s.d)), ("seqlens", i32, (s.B,)),
+                       ("page_table", i32, (s.B, s.max_pages)) if s.page_size else None)
+        self._window = (*self._cache, ("q", bf16, heads), ("out", f32, heads), ("lse", f32, (s.B, s.Hq)), ("weights", f32, positions))
+        self._evict = (*self._cache, ("weights", f32, positions), ("keep", i32, (s.B,)), ("log_g", f32, positions), ("idx", i32, (s.B, s.Hkv, self.k_max)),
+                       ("weights_out", f32, positions), ("seqlens_out", i32, (s.B,)))
         sizes = [lib.sas_decode_workspace_bytes(shape, self.k_max)]
         if dense:
             sizes.append(lib.sas_dense_workspace_bytes(shape))
@@ -76,42 +92,60 @@ class DecodeSession:
                                  out, self.workspace, self.ws_bytes)
         return out
 
-    def _run(self, call, tensors, *args):
-        """A call on the session's device and that device's current stream; every tensor lies there."""
+    def _run(self, call, tensors, specs, *args):
+        """A call on the session's device and that device's current stream.  Every tensor lies there and, where
+        there is a spec, has its layout: the library takes addresses, and would read or write another as if it had."""
         index = self.device.index
-        for t in tensors:
-            if t is not None and t.get_device() != index:
-                raise ValueError(f"a tensor lies on {t.device}, the session on {self.device}")
+        for x, spec in zip(tensors, specs):
+            if x is None:
+                continue
+            if x.get_device() != index:
+                raise ValueError(f"a tensor lies on {x.device}, the session on {self.device}")
+            if spec is None:
+                continue
+            name, dtype, shape = spec
+            if (x.shape != shape or x.dtype is not dtype or not x.is_contiguous()) and _other_layout(x, dtype, shape):
+                raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {x.dtype} {list(x.shape)} with strides {x.stride()}")
         if torch.cuda.current_device() == index:
             call(self.shape, *args, self.workspace, self.ws_bytes, lib._raw_stream(index))
         else:
             with torch.cuda.device(index):
                 call(self.shape, *args, self.workspace, self.ws_bytes, lib._raw_stream(index))
 
+    def _projected(self, Kproj):
+        """Spec of projected rows, as values or as their bytes."""
+        if Kproj is None:
+            return None
+        row = self.shape.r * (1 if self.shape.kproj_dtype == lib.SAS_KPROJ_FP8_E4M3 else 2)
+        return ("Kproj", Kproj.dtype, (*self._rows, row // Kproj.element_size()))
+
     def append_chunk(self, K_new, V_new, q_start, M, K, V, Kproj, page_table, seqlens):
         """K_new, V_new [n_new][Hkv][d], tokens at any stride; Kproj (and M) may be None."""
         n_new, stride = _tokens(K_new, self.shape.Hkv, self.shape.d, "K_new")
         if _tokens(V_new, self.shape.Hkv, self.shape.d, "V_new") != (n_new, stride):
             raise ValueError("K_new and V_new differ in tokens or stride")
-        self._run(lib.sas_append_chunk, (K_new, V_new, q_start, M, K, V, Kproj, page_table, seqlens), K_new, V_new, stride,
-                  q_start, n_new, M, K, V, Kproj, page_table, seqlens)
+        self._run(lib.sas_append_chunk, (K, V, seqlens, page_table, q_start, M, Kproj, K_new, V_new),
+                  (*self._cache, self._starts, self._m, self._projected(Kproj), None, None),
+                  K_new, V_new, stride, q_start, n_new, M, K, V, Kproj, page_table, seqlens)
 
     def chunk(self, q, q_start, K, V, page_table, seqlens, window=0, sinks=0, out=None, lse=None):
         """q [n_new][Hq][d], tokens at any stride.  Returns out (bf16) and lse (None unless given)."""
-        n_new, stride = _tokens(q, self.shape.Hq, self.shape.d, "q")
+        Hq, d = self.shape.Hq, self.shape.d
+        n_new, stride = _tokens(q, Hq, d, "q")
         if n_new > self.chunk_max:
             raise ValueError(f"{n_new} new tokens, more than the session's {self.chunk_max}")
         if out is None:
-            out = torch.empty(n_new, self.shape.Hq, self.shape.d, dtype=torch.bfloat16, device=q.device)
-        self._run(lib.sas_chunk_attention, (q, q_start, K, V, page_table, seqlens, out, lse), q, stride, q_start, n_new, K, V,
-                  page_table, seqlens, window, sinks, out, lse)
+            out = torch.empty(n_new, Hq, d, dtype=torch.bfloat16, device=q.device)
+        self._run(lib.sas_chunk_attention, (K, V, seqlens, page_table, q_start, out, lse, q),
+                  (*self._cache, self._starts, ("out", torch.bfloat16, (n_new, Hq, d)), ("lse", torch.float32, (n_new, Hq)), None),
+                  q, stride, q_start, n_new, K, V, page_table, seqlens, window, sinks, out, lse)
         return out, lse
 
     def window(self, q, K, V, page_table, seqlens, window, sinks=0, weights=None, out=None, lse=None):
-        """The newest token of every sequence.  Adds the softmax weights to `weights` unless None."""
+        """The newest token of every sequence, q dense.  Adds the softmax weights to `weights` unless None."""
         out = self.out if out is None else out
-        self._run(lib.sas_window_decode, (q, K, V, page_table, seqlens, weights, out, lse), q, K, V, page_table, seqlens,
-                  window, sinks, out, lse, weights)
+        self._run(lib.sas_window_decode, (K, V, seqlens, page_table, q, out, lse, weights), self._window,
+                  q, K, V, page_table, seqlens, window, sinks, out, lse, weights)
         return out, lse
 
     def evict(self, weights, keep, sinks, recent, K, V, Kproj, log_g, page_table, seqlens, idx=None, weights_out=None,
@@ -120,7 +154,8 @@ class DecodeSession:
         idx = self.idx if idx is None else idx
         weights_out = weights if weights_out is None else weights_out
         seqlens_out = seqlens if seqlens_out is None else seqlens_out
-        self._run(lib.sas_evict, (weights, keep, K, V, Kproj, log_g, page_table, seqlens, idx, weights_out, seqlens_out),
+        self._run(lib.sas_evict, (K, V, seqlens, page_table, weights, keep, log_g, idx, weights_out, seqlens_out, Kproj),
+                  (*self._evict, self._projected(Kproj)),
                   weights, keep, self.k_max, sinks, recent, K, V, Kproj, log_g, page_table, seqlens, idx, weights_out,
                   seqlens_out)
         return idx
