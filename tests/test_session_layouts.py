@@ -1,14 +1,16 @@
-"""DecodeSession refuses tensors whose type, extents or strides are not what the library reads.
+"""DecodeSession refuses tensors whose type, extents or strides are not what the library reads, and works
+on its own device whatever the current one is.
 
 The library takes addresses: a tensor of another layout would be read, or written, as if it had the
 right one.  On the CPU, with the library's calls recorded instead of made.
 """
 import contextlib
+import types
 
 import pytest
 import torch
 
-from token_level_sparse_head_b200 import DecodeSession, Shape, lib
+from token_level_sparse_head_b200 import DecodeSession, Shape, lib, session
 
 BF, F, I = torch.bfloat16, torch.float32, torch.int32
 CALLS = {"append_chunk": "sas_append_chunk", "chunk": "sas_chunk_attention", "window": "sas_window_decode", "evict": "sas_evict"}
@@ -116,3 +118,35 @@ def test_queries_of_a_fused_projection(made):
     with pytest.raises(ValueError, match="q must be contiguous"):
         s.window(**dict(args["window"], q=fused[:3, :8]))
     assert made == ["sas_chunk_attention"]
+
+
+def test_every_call_is_made_on_the_sessions_device(monkeypatch):
+    """The workspace is cleared, used and read back on streams of the device that it lies on."""
+    current, made = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        was, current[0] = current[0], (7 if isinstance(d, torch.device) else d)
+        yield
+        current[0] = was
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(lib, "_raw_stream", lambda index: 100 + index)
+    for name in ("sas_workspace_init", "sas_check_workspace"):
+        monkeypatch.setattr(lib, name, lambda *a, name=name: made.append((name, current[0], 100 + current[0])))
+    for name in (*CALLS.values(), "sas_decode_step", "sas_dense_decode", "sas_select_topk", "sas_sparse_attention"):
+        # without a stream the library takes the current device's
+        monkeypatch.setattr(lib, name, lambda *a, name=name: made.append((name, current[0], a[-1] if isinstance(a[-1], int) and a[-1] >= 100 and
+                                                                            a[-1] < 200 else 100 + current[0])))
+    s = DecodeSession(Shape(1, 2, 1, 64, 16, 256), 4, device="cpu", chunk=2, window=True, evict=True)
+    s.device = torch.device("cuda", 7)
+    x = types.SimpleNamespace(get_device=lambda: 7, shape=(), dtype=None, is_contiguous=lambda: True, stride=tuple, device="cuda:7")
+    monkeypatch.setattr(session, "_other_layout", lambda *a: False)
+    monkeypatch.setattr(session, "_tokens", lambda *a: (2, 128))
+    s._projected = lambda kp: None
+    s.decode(x, x, x, x, x, None, x, x), s.dense(x, x, x, None, x), s.select(x, x, x, None, x, x), s.attend(x, x, x, None, x, x, x)
+    s.append_chunk(x, x, x, x, x, x, x, None, x), s.chunk(x, x, x, x, None, x, out=x), s.window(x, x, x, None, x, 0, out=x)
+    s.evict(x, x, 0, 0, x, x, x, x, None, x, idx=x)
+    s.check()
+    assert len(made) == 10 and {m[1:] for m in made} == {(7, 107)}, made

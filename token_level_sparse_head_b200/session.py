@@ -63,38 +63,45 @@ class DecodeSession:
         nbytes = max(sizes)
         self.ws_bytes = nbytes
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        lib.sas_workspace_init(self.workspace, nbytes)
         self.device = self.workspace.device
+        with torch.cuda.device(self.device):
+            lib.sas_workspace_init(self.workspace, nbytes)
         self.out = torch.empty(shape.B, shape.Hq, shape.d, dtype=torch.float32, device=device)
         self.idx = torch.empty(shape.B, shape.Hkv, self.k_max, dtype=torch.int32, device=device)
 
     def decode(self, q, M, Kproj, K, V, page_table, seqlens, k, lam=0.0, log_g=None, out=None, idx=None):
         out = self.out if out is None else out
         idx = self.idx if idx is None else idx
-        lib.sas_decode_step(self.shape, q, M, Kproj, K, V, page_table, seqlens, k, self.k_max, lam, log_g,
-                            out, idx, self.workspace, self.ws_bytes)
+        self._launch(lib.sas_decode_step, q, M, Kproj, K, V, page_table, seqlens, k, self.k_max, lam, log_g, out, idx)
         return out, idx
 
     def dense(self, q, K, V, page_table, seqlens, out=None):
         out = self.out if out is None else out
-        lib.sas_dense_decode(self.shape, q, K, V, page_table, seqlens, out, self.workspace, self.ws_bytes)
+        self._launch(lib.sas_dense_decode, q, K, V, page_table, seqlens, out)
         return out
 
     def select(self, q, M, Kproj, page_table, seqlens, k, lam=0.0, log_g=None, idx=None, scores=None):
         idx = self.idx if idx is None else idx
-        lib.sas_select_topk(self.shape, q, M, Kproj, page_table, seqlens, k, self.k_max, lam, log_g, idx,
-                            scores, self.workspace, self.ws_bytes)
+        self._launch(lib.sas_select_topk, q, M, Kproj, page_table, seqlens, k, self.k_max, lam, log_g, idx, scores)
         return idx
 
     def attend(self, q, K, V, page_table, seqlens, idx, k, lam=0.0, log_g=None, out=None):
         out = self.out if out is None else out
-        lib.sas_sparse_attention(self.shape, q, K, V, page_table, seqlens, idx, k, self.k_max, lam, log_g,
-                                 out, self.workspace, self.ws_bytes)
+        self._launch(lib.sas_sparse_attention, q, K, V, page_table, seqlens, idx, k, self.k_max, lam, log_g, out)
         return out
 
+    def _launch(self, call, *args):
+        """A call on the session's device and that device's current stream."""
+        index = self.device.index
+        if torch.cuda.current_device() == index:
+            call(self.shape, *args, self.workspace, self.ws_bytes, lib._raw_stream(index))
+        else:
+            with torch.cuda.device(index):
+                call(self.shape, *args, self.workspace, self.ws_bytes, lib._raw_stream(index))
+
     def _run(self, call, tensors, specs, *args):
-        """A call on the session's device and that device's current stream.  Every tensor lies there and, where
-        there is a spec, has its layout: the library takes addresses, and would read or write another as if it had."""
+        """A call whose tensors all lie on the session's device and, where there is a spec, have its layout: the
+        library takes addresses, and would read or write another as if it had."""
         index = self.device.index
         for x, spec in zip(tensors, specs):
             if x is None:
@@ -106,11 +113,7 @@ class DecodeSession:
             name, dtype, shape = spec
             if (x.shape != shape or x.dtype is not dtype or not x.is_contiguous()) and _other_layout(x, dtype, shape):
                 raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {x.dtype} {list(x.shape)} with strides {x.stride()}")
-        if torch.cuda.current_device() == index:
-            call(self.shape, *args, self.workspace, self.ws_bytes, lib._raw_stream(index))
-        else:
-            with torch.cuda.device(index):
-                call(self.shape, *args, self.workspace, self.ws_bytes, lib._raw_stream(index))
+        self._launch(call, *args)
 
     def _projected(self, Kproj):
         """Spec of projected rows, as values or as their bytes."""
@@ -162,4 +165,5 @@ class DecodeSession:
 
     def check(self):
         """(status, code, where) of the device-side checks since the last check (synchronises)."""
-        return lib.sas_check_workspace(self.workspace, self.ws_bytes)
+        with torch.cuda.device(self.device):
+            return lib.sas_check_workspace(self.workspace, self.ws_bytes)
