@@ -51,6 +51,11 @@ constexpr int kRowsCap = 2 * kTile;  // rows of a partial
 // (512 tokens on 32K rows, 128 MB: one wave 284 us, two 264 us, three 280 us).
 constexpr long long kLiveBytes = 72LL << 20;
 constexpr int kWaveUnits = 24;       // units of a CTA and wave that a partial per wave is worth
+// The matrix instruction truncates its sums, always towards zero (about 2^-23 of the running output
+// a step: 262144 rows in one go came out 1.0e-3 low on average, as much as a quarter of bf16's step),
+// so an output is summed in tensor memory over this many units at most and then added, with rounding,
+// to a sum in the CTA's partial.  4096 tokens on 128K rows take 7.3 ms without, 7.6 with 128 or 256.
+constexpr int kFoldUnits = 128;
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D>
@@ -610,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < kTile / 16; ++i)
               mma_ts(tmem + Gm::COL_O + x * D, tmem + Gm::COL_P + x * (kTile / 2) + i * 8, b + i * (2048 >> 4), kFormO,
-                     j > 0 || i > 0, lead);
+                     (j & (kFoldUnits - 1)) > 0 || i > 0, lead);
             tc_commit(&pv_done[x], lead);
             if (one || x == 1) tc_commit(&empty[v.st], lead);
           }
@@ -747,7 +752,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               wait_row(&pv_done[x], ph_o, &stop_s);
               ph_o ^= 1;
               tc_fence_after();
-              if (grow) {
+              if ((j & (kFoldUnits - 1)) == 0) {
+                // O moves to the partial; its maximum there is the one of now
+                const int slot = 2 * (w * p.ctas + (int)blockIdx.x) + (first ? 0 : 1), at = x * kTile + r;
+                float4* part = reinterpret_cast<float4*>(p.part) + (size_t)slot * (D / 4) * kRowsCap + at;
+                float* was = &p.ml[(size_t)slot * kRowsCap + at].x;
+                const float g = j == kFoldUnits || *was == -INFINITY ? 0.f : ex2((*was - m) * scale);
+#pragma unroll 1
+                for (int i = 0; i < D / 8; ++i) {
+                  float o[8];
+                  tmem_ld8(o, tO + 8 * i);
+                  float4 y[2] = {};
+                  if (j > kFoldUnits) {
+                    y[0] = part[(size_t)(2 * i) * kRowsCap];
+                    y[1] = part[(size_t)(2 * i + 1) * kRowsCap];
+                  }
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    part[(size_t)(2 * i + e) * kRowsCap] = make_float4(y[e].x * g + o[4 * e] * f, y[e].y * g + o[4 * e + 1] * f,
+                                                                       y[e].z * g + o[4 * e + 2] * f, y[e].w * g + o[4 * e + 3] * f);
+                }
+                *was = m;
+                __syncwarp();
+              } else if (grow) {
 #pragma unroll 1
                 for (int i = 0; i < D / 8; ++i) {  // 8 columns at a time: the scores stay in registers
                   float o[8];
@@ -792,21 +820,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         tc_fence_after();
         const GroupSeg g(p, list_s, c, x);
         const bool done = n == g.t.blocks;
-        const int slot = 2 * (w * p.ctas + (int)blockIdx.x) + (first ? 0 : 1);
+        const int slot = 2 * (w * p.ctas + (int)blockIdx.x) + (first ? 0 : 1), at = x * kTile + r;
         float4* part = reinterpret_cast<float4*>(p.part) + (size_t)slot * (D / 4) * kRowsCap;
         float2* ml = p.ml + (size_t)slot * kRowsCap;
         const float mz = m == -INFINITY ? m : m * scale;
+        // what the partial holds already of a long segment's outputs
+        const bool folded = n > kFoldUnits;
+        const float fold = !folded || ml[at].x == -INFINITY ? 0.f : ex2((ml[at].x - m) * scale);
+        auto add_folded = [&](float (&o)[32], int i) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 y = part[(size_t)(8 * i + e) * kRowsCap + at];
+            o[4 * e] += y.x * fold;
+            o[4 * e + 1] += y.y * fold;
+            o[4 * e + 2] += y.z * fold;
+            o[4 * e + 3] += y.w * fold;
+          }
+        };
         if (!done || (one && x == 1)) {
           // the other warpgroup has read the half it got before
           if (done && half_used) wait_row(&half_free, ph_half ^ 1, &stop_s);
           if (busy) {
-            const int at = x * kTile + r;
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
               float o[32];
               tmem_ld32(o, tO + 32 * i);
               tmem_wait_ld();
               if (mine) {
+                if (folded) add_folded(o, i);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                   part[(size_t)(8 * i + e) * kRowsCap + at] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -846,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               tmem_ld32(o, tO + 32 * i);
               tmem_wait_ld();
               if (mine) {
+                if (folded) add_folded(o, i);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] *= f0;
                 if (one) {
