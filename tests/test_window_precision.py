@@ -1,4 +1,5 @@
-"""The window decode's fp32 outputs: that the weights keep their 24 bits and the sums are rounded.
+"""The window decode's fp32 outputs: that the weights keep their 24 bits and the sums are rounded; and the
+longest list of pages that it can cut into shares.
 
 The bounds here are those of single roundings, not of a whole softmax, so fewer bits anywhere show.
 """
@@ -7,7 +8,7 @@ import pytest
 import torch
 
 from tests.helpers import f64
-from token_level_sparse_head_b200 import DecodeSession, Shape
+from token_level_sparse_head_b200 import DecodeSession, Shape, lib
 
 U = 2.0 ** -24
 
@@ -61,3 +62,13 @@ def test_sums_of_many_rows_are_rounded(cuda_lib, d, Hq):
     off = out.double() / V.double().mean(0) - 1
     assert off.abs().max() <= 79 * U and off.mean().abs() <= 1e-6, (off.abs().max(), off.mean())
     assert (lse.double() - np.log(n)).abs().max() <= 2.0 ** -21 * (1 + np.log(n))
+
+
+def test_a_list_of_pages_that_32_bits_cannot_share_out():
+    """524160 head groups of 4097 pages: 128 below 2^31, where a share rounded up times the last CTA passes it."""
+    groups, at = 524160, 1 << 20
+    assert 0 < 2 ** 31 - groups * (262144 // 64 + 1) < 148
+    shape = Shape(1, 16 * groups, 1, 64, 16, n_cap=262144)
+    with pytest.raises(lib.SasError) as e:
+        lib.sas_window_decode(shape, at, at, at, None, at, 0, 0, at, at, None, at, 1 << 40, 0)
+    assert e.value.status == lib.SAS_ERR_UNSUPPORTED

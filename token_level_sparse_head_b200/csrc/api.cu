@@ -795,8 +795,9 @@ sas_status sas_window_decode(const sas_shape* shape, const void* q, const void* 
   SAS_TRY(check_ptr(weights, "weights", false));
   SAS_TRY(check_cache_ptrs(shape, page_table, seqlens));
   sas::WindowParams p = window_plan(shape, window, sinks);
-  if ((long long)p.B * p.Hkv * p.hgs * (p.cap / 64 + 1) >= (1LL << 31))
-    return fail(SAS_ERR_UNSUPPORTED, "pages times head groups exceed 2^31");
+  // a CTA's number times its share, rounded up, stays an int
+  if ((long long)p.B * p.Hkv * p.hgs * (p.cap / 64 + 1) >= (1LL << 31) - sas::kChunkMaxCtas)
+    return fail(SAS_ERR_UNSUPPORTED, "pages times head groups exceed 2^31 - %d", sas::kChunkMaxCtas);
   SAS_TRY(check_ws(workspace, ws_bytes, sas_window_workspace_bytes(shape, weights != nullptr)));
   unsigned char* w = static_cast<unsigned char*>(workspace);
   sas::bind_window(p, w + scratch_offset(shape), weights != nullptr);
