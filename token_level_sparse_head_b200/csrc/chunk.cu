@@ -44,13 +44,23 @@ namespace {
 constexpr int kPage = 64;
 constexpr int kThreads = 384;      // 8 softmax warps, 1 matrix warp, 1 load warp, 2 idle: three warpgroups
 constexpr int kPlanThreads = 1024;
-constexpr int kOwnPlanSlots = 256;   // up to so many task slots every CTA makes the list itself
+// Up to so many task slots every CTA makes the list itself, which saves a kernel (64 tokens of 64
+// sequences of 1K rows: 106 us, with the kernel 112; of 250 sequences, 500 slots, 375 and 381).  More
+// would gain 1 % (1125 slots: 899 and 910 us) for 40 bytes a slot and CTA of workspace.
+constexpr int kOwnPlanSlots = 256;
 constexpr int kTile = 128;
 constexpr int kRowsCap = 2 * kTile;  // rows of a partial
-// K and V bytes of a wave: more do not stay in the 126 MB of L2, fewer waves leave fewer partials
-// (512 tokens on 32K rows, 128 MB: one wave 284 us, two 264 us, three 280 us).
+// K and V bytes of a wave: more do not stay in the 126 MB of L2, fewer bytes are more waves, each of
+// which leaves partials.  Under steady load, where HBM traffic costs clock (32 heads, 8 KV heads): 512
+// tokens on 32K rows (128 MB) in one wave 298 us, in two 266; 1024 on 64K in waves of 64 MB 951, of
+// 86 MB 989; with d = 64 512 on 64K in waves of 32 MB 377, of 64 MB 370, in one 390.  (A call by itself,
+// at full clock, is faster in one wave: 512 on 32K 240 and 250 us.)
 constexpr long long kLiveBytes = 72LL << 20;
-constexpr int kWaveUnits = 24;       // units of a CTA and wave that a partial per wave is worth
+// Units of a CTA and wave that a partial per wave is worth.  At 24 to 47 units two waves lose: 256 tokens
+// on 32K rows 168 us, in one wave 156; 384 on 32K 220 and 204; 128 on 64K 199 and 164.  At 48 to 99 they
+// gain: 512 on 32K 275 and 298 (one), 256 on 64K 298 and 312, 512 on 64K in three 540, in two 568.
+constexpr int kWaveUnits = 48;
+
 // The matrix instruction truncates its sums, always towards zero (about 2^-23 of the running output
 // a step: 262144 rows in one go came out 1.0e-3 low on average, as much as a quarter of bf16's step),
 // so an output is summed in tensor memory over this many units at most and then added, with rounding,
