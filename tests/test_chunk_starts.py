@@ -133,7 +133,7 @@ def run_append(p, start, lens, n_new, with_proj):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("paged", [True, False])
-@pytest.mark.parametrize("Hkv,d", [(2, 64), (40, 128)])   # a CTA per token and head; tiles of tokens
+@pytest.mark.parametrize("Hkv,d", [(2, 64), (56, 128)])   # a CTA per token and head; tiles of tokens
 @pytest.mark.parametrize("start,lens,codes", STARTS)
 def test_append_skips(cuda_lib, start, lens, codes, Hkv, d, paged):
     p = make_problem(B=4, Hq=Hkv, Hkv=Hkv, d=d, r=16, seqlens=LENS, k=1, paged=paged, seed=4)
@@ -152,7 +152,7 @@ def test_append_skips_in_a_large_batch(cuda_lib, Hkv, most):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("Hkv", [2, 40])
+@pytest.mark.parametrize("Hkv", [2, 56])
 def test_append_reports_a_page_outside_the_cache(cuda_lib, Hkv):
     p = make_problem(B=4, Hq=Hkv, Hkv=Hkv, d=64, r=16, seqlens=LENS, k=1, paged=True, seed=4)
     c = p.to("cuda")

@@ -16,8 +16,8 @@
 //                 single ones).
 // What bounds the tiles: moving K and V of 8192 tokens and 8 heads (67 MB in and out) takes 9.6 us
 // alone, the call with 32 outputs per row 26 us: 268 M fp32 FMAs are 7.5 us at full rate, and the
-// conversions and loads of their operands as much again.  The tensor cores would need another
-// summation order, and rows would then depend on the call that wrote them.
+// conversions and loads of their operands as much again.  A form on the matrix instructions would
+// have to be the build's and the one-token append's too, for the rows to stay the same bits.
 #include <cuda_fp8.h>
 
 #include "sas_device.cuh"
@@ -144,6 +144,12 @@ __global__ void __launch_bounds__(256) token_kernel(const AppendParams p) {
 
 constexpr int kTileTokens = 128;
 constexpr int kTileThreads = 256;
+// Up to so many (token, head) pairs an SM a CTA each; beyond it tiles, whose first round takes the same
+// time whatever share of the SMs it fills.  8 heads, d = 128, r = 32: 140 tokens 5.3 us in pairs and 9.0
+// in tiles, 256 tokens (13.8 pairs an SM) 8.8 and 9.2, 320 tokens 10.0 and 9.2, 512 14.1 and 9.2; the
+// same crossing with r = 64 (256 tokens 13.5 and 13.9, 320 15.6 and 13.7), with d = 64 and r = 16 (4.7
+// and 4.7, 5.5 and 4.7) and with one head (2000 tokens 8.4 and 9.2, 2300 9.2 and 9.2).
+constexpr long long kPairsPerSm = 14;
 
 template <int D, int R>
 struct TileSmem {
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(const AppendParam
 template <int D, int R, bool FP8>
 cudaError_t launch_drf(const AppendParams& p, int sms, cudaStream_t stream) {
   const long long pairs = (long long)p.n_new * p.Hkv;
-  if (pairs <= 8LL * sms)
+  if (pairs <= kPairsPerSm * sms)
     return launch_pdl(token_kernel<D, R, FP8>, dim3((unsigned)pairs), dim3(256), 0, stream, p);
   auto kern = tile_kernel<D, R, FP8>;
   const int smem = (int)sizeof(TileSmem<D, R>);
