@@ -176,18 +176,10 @@ __device__ __forceinline__ void wait_row(uint64_t* bar, uint32_t parity, volatil
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* stop) {
   return __all_sync(0xffffffffu, wait_live(bar, parity, stop));
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 // The softmax threads hold a row of 128 scores; the launch's 384 x 168 registers are dealt out
 // again as 2 x 128 x 208 + 128 x 88.
@@ -676,6 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const int pj = g.vis.page(v) * kPage + (r & 63);
           const bool clear = v < g.vis.nv && (pj >= g.t.seqlen || (pj < g.vis.first && pj >= p.sinks));
           if (__any_sync(0xffffffffu, clear)) {
+            // The parity tells this turn of the place from the next one only if the block one turn
+            // earlier has landed: it is this unit's K or lies before it, which the matrix warp, taking
+            // all blocks in order, had waited for before these scores.
             const int idx = base + ring_v(one, j, x, n), st = idx % ST;
             wait_row(&full[st], (idx / ST) & 1, &stop_s);
             if (clear) {

@@ -92,9 +92,6 @@ static_assert(smem_fits<16, 128, true, true>() && smem_fits<32, 128, true, true>
 __device__ __forceinline__ void stg_hint(uint32_t* ptr, uint32_t v, uint64_t pol) {
   asm volatile("st.global.L2::cache_hint.u32 [%0], %1, %2;" ::"l"(ptr), "r"(v), "l"(pol) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 // Barrier 1 among the consumer warps (the producer warp never joins it).
 template <int N>
 __device__ __forceinline__ void consumers_sync() {
