@@ -150,3 +150,15 @@ def test_every_call_is_made_on_the_sessions_device(monkeypatch):
     s.evict(x, x, 0, 0, x, x, x, x, None, x, idx=x)
     s.check()
     assert len(made) == 10 and {m[1:] for m in made} == {(7, 107)}, made
+
+
+def test_the_scale_is_the_shapes_of_now(made, monkeypatch):
+    """The C structure is made once; a scale tensor that the caller puts in later is the one that calls get."""
+    s, args = make(True, fp8=True)
+    seen = []
+    monkeypatch.setattr(lib, "sas_append_chunk", lambda shape, *a: seen.append((shape.c().kproj_scale, shape.c().B)))
+    first = s.shape.kproj_scale
+    s.append_chunk(**args["append_chunk"])
+    s.shape.kproj_scale = torch.full_like(first, 2.0)
+    s.append_chunk(**args["append_chunk"])
+    assert seen == [(first.data_ptr(), 3), (s.shape.kproj_scale.data_ptr(), 3)]
