@@ -15,7 +15,7 @@
 //                 A thread takes 4 outputs of 4 tokens in paired fp32 FMAs (bit-identical to
 //                 single ones).
 // What bounds the tiles: moving K and V of 8192 tokens and 8 heads (67 MB in and out) takes 9.6 us
-// alone, the call with 32 outputs per row 26 us: 268 M fp32 FMAs are 7.5 us at full rate, and the
+// alone, the call with 32 outputs per row 26.5 us: 268 M fp32 FMAs are 7.5 us at full rate, and the
 // conversions and loads of their operands as much again.  A form on the matrix instructions would
 // have to be the build's and the one-token append's too, for the rows to stay the same bits.
 #include <cuda_fp8.h>

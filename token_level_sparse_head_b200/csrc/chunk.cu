@@ -26,12 +26,12 @@
 // K and V blocks of 128 keys pass through one ring of tiled bulk copies (128-byte swizzle).
 //
 // What bounds it, for two-tile units with d = 128: a unit is 2048 cycles of matrix instructions and
-// takes about 2900.  Shared memory gives 128 bytes a cycle and Q K^T alone takes that, so every
-// byte the copies write (64 KB a unit) and V's reads stretch it; with the softmax left out a unit
-// still took 2800.  Measured: prompt of 8192 (32 heads, 8 KV heads) 561 us, 980 TFLOP/s; 512 tokens
-// on 32K rows 265 us, 1030 TFLOP/s, both at the 1.1-1.3 GHz that the power limit leaves; 8 x 5
-// tokens on 4K to 32K rows 116 us, 5.2 TB/s.  With d = 64 the loop over blocks (3100 cycles) and the
-// ends of tasks (4000 each) bound it.
+// takes about 2940.  No unit of the SM is full: matrix pipe 69 %, special functions 70 %, shared memory
+// about 2040 of the 2940 cycles (1527 wavefronts of operands, 512 of copies); the tiles share one S and
+// take turns, and with the softmax left out a unit still took 2800.  Measured: prompt of 8192 (32 heads,
+// 8 KV heads) 562 us, 980 TFLOP/s; 512 tokens on 32K rows 262 to 266 us, 1030 TFLOP/s, both at the 1.1-1.3
+// GHz that the power limit leaves; 8 x 5 tokens on 4K to 32K rows 112 to 117 us, 5.2 TB/s.  With d = 64
+// the loop over blocks (3100 cycles) and the ends of tasks (4000 each) bound it.
 // Tried and not kept: a warp for each of the two products (384K cycles against 345K for 512 on
 // 32K); polynomial exponentials on the FMA pipe for part of the row (286 us without, 288 to 316 us
 // with); P in the place of S (a tile's products then wait for its softmax).

@@ -13,7 +13,7 @@
 // before it has set its flag, so every wait ends.  The reads and writes of all segments are thus
 // in flight together; a CTA that went through a column slice of all rows in order, with no flags,
 // took 581 us for the 1.2 GB of a batch of 16 (8K to 128K rows, an eighth kept), this form 256 us
-// (4.9 TB/s); for one sequence of 32K 28.8 against 13 us.
+// (4.9 TB/s); for one sequence of 32K 28.8 against 13.7 us.
 #include "sas_device.cuh"
 #include "sas_kernels.h"
 

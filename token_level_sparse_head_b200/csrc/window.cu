@@ -17,8 +17,8 @@
 // the second product as three bf16 terms of 8 bits each, which hold its 24 bits exactly, because
 // the output is fp32: one bf16 term would be off by up to 2^-8, two by 2^-16.
 // Measured (8 KV heads, d = 128): window 4096 at B = 16 52 us, 5.2 TB/s; whole caches of 4 x 64K rows
-// with weights 200 us, 5.4 TB/s, of which the weights' own pass takes 13; window 1024 at B = 1 9.2 us,
-// where the chain of page, products and join counts and not the bytes.
+// with weights 197 to 200 us, 5.5 TB/s, of which the weights' own pass takes 13; window 1024 at B = 1 9.7
+// us, host time; the kernel's chain of page, products and join counts there and not the bytes.
 #include "sas_device.cuh"
 #include "sas_kernels.h"
 
