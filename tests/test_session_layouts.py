@@ -161,4 +161,6 @@ def test_the_scale_is_the_shapes_of_now(made, monkeypatch):
     s.append_chunk(**args["append_chunk"])
     s.shape.kproj_scale = torch.full_like(first, 2.0)
     s.append_chunk(**args["append_chunk"])
-    assert seen == [(first.data_ptr(), 3), (s.shape.kproj_scale.data_ptr(), 3)]
+    second, s.shape.kproj_scale = s.shape.kproj_scale, None
+    s.append_chunk(**args["append_chunk"])  # which the library then refuses
+    assert seen == [(first.data_ptr(), 3), (second.data_ptr(), 3), (None, 3)]

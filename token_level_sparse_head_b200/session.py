@@ -34,9 +34,7 @@ class _Sizes:
         self.shape, self._c = shape, shape.c()
 
     def c(self):
-        scale = self.shape.kproj_scale
-        if scale is not None:
-            self._c.kproj_scale = lib._p(scale)
+        self._c.kproj_scale = lib._p(self.shape.kproj_scale)
         return self._c
 
 
