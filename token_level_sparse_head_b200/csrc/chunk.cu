@@ -762,7 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 const int slot = 2 * (w * p.ctas + (int)blockIdx.x) + (first ? 0 : 1), at = x * kTile + r;
                 float4* part = reinterpret_cast<float4*>(p.part) + (size_t)slot * (D / 4) * kRowsCap + at;
                 float* was = &p.ml[(size_t)slot * kRowsCap + at].x;
-                const float g = j == kFoldUnits || *was == -INFINITY ? 0.f : ex2((*was - m) * scale);
+                const float m0 = j == kFoldUnits ? -INFINITY : *was;
+                const float g = ex2((m0 == -INFINITY ? m0 : m0 - m) * scale);  // a select: the warp stays together
 #pragma unroll 1
                 for (int i = 0; i < D / 8; ++i) {
                   float o[8];
@@ -831,7 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const float mz = m == -INFINITY ? m : m * scale;
         // what the partial holds already of a long segment's outputs
         const bool folded = n > kFoldUnits;
-        const float fold = !folded || ml[at].x == -INFINITY ? 0.f : ex2((ml[at].x - m) * scale);
+        const float m0 = folded ? ml[at].x : -INFINITY;
+        const float fold = ex2((m0 == -INFINITY ? m0 : m0 - m) * scale);
         auto add_folded = [&](float (&o)[32], int i) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
